@@ -3,6 +3,7 @@ step of the path runs in the library. The binding refuses to work without the
 compiled library; there is no fallback of any kind."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -21,6 +22,7 @@ PCP_ERR_ALIGN = -4
 PCP_ERR_CUDA = -5
 PCP_ERR_TIMEOUT = -6
 PCP_ERR_WORKSPACE = -7
+PCP_ERR_PAGES = -8
 
 PCP_SPLIT_CONTIGUOUS = 0
 PCP_SPLIT_DUAL_CHUNK = 1
@@ -41,11 +43,16 @@ def PCP_ATTN_DECODE_SMS(n: int) -> int:
     return (int(n) & 0xFF) << 16
 
 ROW_FIELDS = ("req", "shard", "q_start", "q_len", "ctx_len", "kv_end", "causal_off", "is_decode")
+PREFIX_FIELDS = ("q_start", "q_len", "req", "prefix_len")
 
 # every symbol include/pcp.h declares
 EXPORTS = ("pcp_build_row_plan", "pcp_mask_slots_for_shard", "pcp_decode_sms", "pcp_kv_cache_write",
            "pcp_kv_cache_write_fp8", "pcp_attn_workspace_size", "pcp_attn_varlen", "pcp_attn_varlen_noalloc",
            "pcp_attn_varlen_fp8kv", "pcp_lse_merge",
+           "pcp_attn_window_workspace_size", "pcp_attn_window", "pcp_attn_window_fp8kv",
+           "pcp_build_prefix_groups", "pcp_attn_shared_prefix_workspace_size", "pcp_attn_shared_prefix",
+           "pcp_attn_shared_prefix_fp8kv", "pcp_kv_pages_workspace_size", "pcp_kv_fork", "pcp_kv_release",
+           "pcp_kv_compact",
            "pcp_set_profile_events", "pcp_selftest_bounded_wait",
            "pcp_last_cuda_error", "pcp_status_string")
 
@@ -98,6 +105,32 @@ def load(path: Optional[str] = None):
     lib.pcp_attn_varlen_noalloc.argtypes = [P, P, P, P, i32, i32, i64, i32, P, i32, i32, i32, i32, i32, f32,
                                             P, P, i32, P, P]
     lib.pcp_attn_varlen_noalloc.restype = ctypes.c_int
+    lib.pcp_attn_window_workspace_size.argtypes = [i32] * 9
+    lib.pcp_attn_window_workspace_size.restype = sz
+    lib.pcp_attn_window.argtypes = [P, P, P, P, i32, i32, i64, i32, P, i32, i32, i32, i32, i32, f32, i32, i32, P, P,
+                                    P, sz, P, P]
+    lib.pcp_attn_window.restype = ctypes.c_int
+    lib.pcp_attn_window_fp8kv.argtypes = [P, P, P, P, P, P, i32, i32, i64, i32, P, i32, i32, i32, i32, i32, f32, i32,
+                                          i32, P, P, P, sz, P, P]
+    lib.pcp_attn_window_fp8kv.restype = ctypes.c_int
+    lib.pcp_build_prefix_groups.argtypes = [P, i32, P, i32, i32, i32, i32, P, i32, P]
+    lib.pcp_build_prefix_groups.restype = ctypes.c_int
+    lib.pcp_attn_shared_prefix_workspace_size.argtypes = [i32] * 7
+    lib.pcp_attn_shared_prefix_workspace_size.restype = sz
+    lib.pcp_attn_shared_prefix.argtypes = [P, P, P, P, i32, i32, i64, i32, P, i32, P, i32, i32, i32, i32, i32, f32,
+                                           P, P, P, sz, P, P]
+    lib.pcp_attn_shared_prefix.restype = ctypes.c_int
+    lib.pcp_attn_shared_prefix_fp8kv.argtypes = [P, P, P, P, P, P, i32, i32, i64, i32, P, i32, P, i32, i32, i32, i32,
+                                                 i32, f32, P, P, P, sz, P, P]
+    lib.pcp_attn_shared_prefix_fp8kv.restype = ctypes.c_int
+    lib.pcp_kv_pages_workspace_size.argtypes = [i64]
+    lib.pcp_kv_pages_workspace_size.restype = sz
+    lib.pcp_kv_fork.argtypes = [P, P, i64, i32, i32, P, i32, i32, P, P, i32, P, P, P, P, sz, P, P]
+    lib.pcp_kv_fork.restype = ctypes.c_int
+    lib.pcp_kv_release.argtypes = [P, i32, i32, P, P, P, i64, P, P, P, P]
+    lib.pcp_kv_release.restype = ctypes.c_int
+    lib.pcp_kv_compact.argtypes = [P, P, i64, i32, i32, P, i32, i32, P, P, P, P, P, sz, P, P]
+    lib.pcp_kv_compact.restype = ctypes.c_int
     lib.pcp_selftest_bounded_wait.argtypes = [P, ctypes.c_uint32, P]
     lib.pcp_selftest_bounded_wait.restype = ctypes.c_int
     lib.pcp_set_profile_events.argtypes = [P, P, P, P]
@@ -122,6 +155,13 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _on(device: torch.device):
+    """The device of a call's tensors as the current one, where it is another."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _check(rc: int, what: str):
@@ -362,6 +402,246 @@ def pcp_attn_varlen_noalloc(q: torch.Tensor, key_cache: torch.Tensor, value_cach
                                      flags, _t_ptr(status), _stream(stream))
     _check(rc, "pcp_attn_varlen_noalloc")
     return out, lse
+
+
+def pcp_attn_window_workspace_size(num_rows: int, total_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                   max_kv_len: int, block_size: int, window: int, num_sinks: int = 0) -> int:
+    return int(load().pcp_attn_window_workspace_size(num_rows, total_q, num_q_heads, num_kv_heads, head_dim,
+                                                     max_kv_len, block_size, window, num_sinks))
+
+
+def pcp_attn_shared_prefix_workspace_size(num_rows: int, num_prefixes: int, total_q: int, num_q_heads: int,
+                                          num_kv_heads: int, head_dim: int, max_kv_len: int) -> int:
+    return int(load().pcp_attn_shared_prefix_workspace_size(num_rows, num_prefixes, total_q, num_q_heads,
+                                                            num_kv_heads, head_dim, max_kv_len))
+
+
+def _attn_buffers(q, out, lse, workspace, need: int):
+    T, hq, _ = q.shape
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((hq, T), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    return out, lse, workspace
+
+
+def _i32_arg(x, name: str) -> int:
+    v = int(x)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name}: {v} does not fit in 32 bits")
+    return v
+
+
+def _attn_window(what, q, key_cache, value_cache, descales, block_table, rows, scale, window, num_sinks, out, lse,
+                 workspace, status, stream, cache_dtypes):
+    lib = load()
+    T, hq, d, nb, bs, hkv = _check_attn(q, key_cache, value_cache, block_table, rows, out, lse, workspace, status,
+                                        cache_dtypes)
+    R, mb, n_rows = int(block_table.shape[0]), int(block_table.shape[1]), int(rows.shape[0])
+    for t, name in zip(descales, ("k_descale", "v_descale")):
+        _dev(t, name, F32, shape=(R, hkv), device=q.device)
+    window, num_sinks = _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks")
+    need = 0 if workspace is not None else pcp_attn_window_workspace_size(n_rows, T, hq, hkv, d, mb * bs, bs, window,
+                                                                          num_sinks)
+    out, lse, workspace = _attn_buffers(q, out, lse, workspace, need)
+    with _on(q.device):
+        rc = getattr(lib, what)(_t_ptr(q), _t_ptr(key_cache), _t_ptr(value_cache), *map(_t_ptr, descales),
+                                _t_ptr(block_table), R, mb, nb, bs, _t_ptr(rows), n_rows, T, hq, hkv, d, float(scale),
+                                window, num_sinks, _t_ptr(out), _t_ptr(lse), _t_ptr(workspace),
+                                int(workspace.numel() * workspace.element_size()), _t_ptr(status), _stream(stream))
+    _check(rc, what)
+    return out, lse
+
+
+def pcp_attn_window(q: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor, block_table: torch.Tensor,
+                    rows: torch.Tensor, scale: float, window: int, num_sinks: int = 0,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """:func:`pcp_attn_varlen` where a query sees the last ``window`` keys up to its
+    own and the first ``num_sinks`` keys of its request."""
+    return _attn_window("pcp_attn_window", q, key_cache, value_cache, (), block_table, rows, scale, window, num_sinks,
+                        out, lse, workspace, status, stream, BF16)
+
+
+def pcp_attn_window_fp8kv(q: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                          k_descale: torch.Tensor, v_descale: torch.Tensor, block_table: torch.Tensor,
+                          rows: torch.Tensor, scale: float, window: int, num_sinks: int = 0,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                          stream=None):
+    """:func:`pcp_attn_window` over FP8 (e4m3, uint8) caches with fp32 descales
+    ``[num_reqs, Hkv]`` on the device."""
+    return _attn_window("pcp_attn_window_fp8kv", q, key_cache, value_cache, (k_descale, v_descale), block_table, rows,
+                        scale, window, num_sinks, out, lse, workspace, status, stream, FP8_CACHE)
+
+
+def pcp_build_prefix_groups(rows: np.ndarray, block_table, block_size: int, min_prefix_len: int = 1024) -> np.ndarray:
+    """Prefix groups int32 ``[n, 4]`` (``PREFIX_FIELDS``) of a host row plan: runs of
+    rows whose block tables begin with the same pages (host function, no GPU)."""
+    lib = load()
+    r = np.ascontiguousarray(rows, dtype=np.int32)
+    if r.ndim != 2 or (r.shape[0] and r.shape[1] != len(ROW_FIELDS)):
+        raise ValueError(f"rows: shape {r.shape}, expected [n, {len(ROW_FIELDS)}]")
+    bt = block_table.numpy() if isinstance(block_table, torch.Tensor) else block_table
+    bt = np.ascontiguousarray(np.asarray(bt, dtype=np.int32))
+    if bt.ndim != 2:
+        raise ValueError(f"block_table: shape {bt.shape}, expected [num_reqs, max_blocks]")
+    cap = max(1, r.shape[0] // 2)
+    out = np.zeros((cap, len(PREFIX_FIELDS)), dtype=np.int32)
+    n = np.zeros(1, dtype=np.int32)
+    rc = lib.pcp_build_prefix_groups(_np_ptr(r), int(r.shape[0]), _np_ptr(bt), int(bt.shape[0]), int(bt.shape[1]),
+                                     _i32_arg(block_size, "block_size"), _i32_arg(min_prefix_len, "min_prefix_len"),
+                                     _np_ptr(out), cap, _np_ptr(n))
+    _check(rc, "pcp_build_prefix_groups")
+    return out[:int(n[0])]
+
+
+def _attn_shared(what, q, key_cache, value_cache, descales, block_table, rows, prefixes, scale, out, lse, workspace,
+                 status, stream, cache_dtypes):
+    lib = load()
+    T, hq, d, nb, bs, hkv = _check_attn(q, key_cache, value_cache, block_table, rows, out, lse, workspace, status,
+                                        cache_dtypes)
+    _dev(prefixes, "prefixes", I32, shape=(-1, len(PREFIX_FIELDS)), device=q.device)
+    R, mb, n_rows, ng = int(block_table.shape[0]), int(block_table.shape[1]), int(rows.shape[0]), int(prefixes.shape[0])
+    for t, name in zip(descales, ("k_descale", "v_descale")):
+        _dev(t, name, F32, shape=(R, hkv), device=q.device)
+    need = 0 if workspace is not None else pcp_attn_shared_prefix_workspace_size(n_rows, ng, T, hq, hkv, d, mb * bs)
+    out, lse, workspace = _attn_buffers(q, out, lse, workspace, need)
+    with _on(q.device):
+        rc = getattr(lib, what)(_t_ptr(q), _t_ptr(key_cache), _t_ptr(value_cache), *map(_t_ptr, descales),
+                                _t_ptr(block_table), R, mb, nb, bs, _t_ptr(rows), n_rows, _t_ptr(prefixes), ng, T, hq,
+                                hkv, d, float(scale), _t_ptr(out), _t_ptr(lse), _t_ptr(workspace),
+                                int(workspace.numel() * workspace.element_size()), _t_ptr(status), _stream(stream))
+    _check(rc, what)
+    return out, lse
+
+
+def pcp_attn_shared_prefix(q: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                           block_table: torch.Tensor, rows: torch.Tensor, prefixes: torch.Tensor, scale: float,
+                           out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                           stream=None):
+    """:func:`pcp_attn_varlen` of a batch whose token groups share prefixes, each
+    prefix attended once for its group. ``prefixes`` int32 ``[n, 4]`` on the device
+    (:func:`pcp_build_prefix_groups`)."""
+    return _attn_shared("pcp_attn_shared_prefix", q, key_cache, value_cache, (), block_table, rows, prefixes, scale,
+                        out, lse, workspace, status, stream, BF16)
+
+
+def pcp_attn_shared_prefix_fp8kv(q: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                                 k_descale: torch.Tensor, v_descale: torch.Tensor, block_table: torch.Tensor,
+                                 rows: torch.Tensor, prefixes: torch.Tensor, scale: float,
+                                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                                 stream=None):
+    """:func:`pcp_attn_shared_prefix` over FP8 (e4m3, uint8) caches with fp32 descales
+    ``[num_reqs, Hkv]`` on the device (a prefix takes those of its request)."""
+    return _attn_shared("pcp_attn_shared_prefix_fp8kv", q, key_cache, value_cache, (k_descale, v_descale), block_table,
+                        rows, prefixes, scale, out, lse, workspace, status, stream, FP8_CACHE)
+
+
+def pcp_kv_pages_workspace_size(num_blocks: int) -> int:
+    return int(load().pcp_kv_pages_workspace_size(num_blocks))
+
+
+def _check_pages(key_cache, value_cache, block_table, ref_count, status):
+    _dev(key_cache, "key_cache", BF16 + FP8_CACHE, shape=(-1, -1, -1, -1))
+    dev = key_cache.device
+    _dev(value_cache, "value_cache", (key_cache.dtype,), shape=tuple(key_cache.shape), device=dev)
+    nb, bs, hkv, d = (int(x) for x in key_cache.shape)
+    _dev(block_table, "block_table", I32, shape=(-1, -1), device=dev)
+    _dev(ref_count, "ref_count", I32, shape=(nb,), device=dev)
+    _status(status, dev)
+    return dev, nb, bs, hkv * d * key_cache.element_size()
+
+
+def _out_like(t, name: str, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    return _dev(t, name, I32, shape=shape, device=device)
+
+
+def _pages_workspace(workspace, nb: int, device):
+    if workspace is None:
+        return torch.empty(max(pcp_kv_pages_workspace_size(nb), 256), dtype=torch.uint8, device=device)
+    return _dev(workspace, "workspace", device=device)
+
+
+def pcp_kv_fork(key_cache: torch.Tensor, value_cache: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
+                parent: torch.Tensor, ref_count: torch.Tensor, block_table_out: Optional[torch.Tensor] = None,
+                ref_count_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None, stream=None):
+    """Children of requests: child ``i`` shares the full pages of request
+    ``parent[i]`` and gets a new page with a copy of the partly filled last one.
+    ``kv_len`` int32 ``[num_reqs]``, ``parent`` int32 ``[num_children]`` (-1: empty
+    child), ``ref_count`` int32 ``[num_blocks]``. Returns ``(block_table_out
+    [num_children, max_blocks], ref_count_out)``."""
+    lib = load()
+    dev, nb, bs, slot_bytes = _check_pages(key_cache, value_cache, block_table, ref_count, status)
+    R, mb = (int(x) for x in block_table.shape)
+    _dev(kv_len, "kv_len", I32, shape=(R,), device=dev)
+    _dev(parent, "parent", I32, shape=(-1,), device=dev)
+    N = int(parent.shape[0])
+    block_table_out = _out_like(block_table_out, "block_table_out", (N, mb), dev)
+    ref_count_out = _out_like(ref_count_out, "ref_count_out", (nb,), dev)
+    workspace = _pages_workspace(workspace, nb, dev)
+    with _on(dev):
+        rc = lib.pcp_kv_fork(_t_ptr(key_cache), _t_ptr(value_cache), nb, bs, slot_bytes, _t_ptr(block_table), R, mb,
+                             _t_ptr(kv_len), _t_ptr(parent), N, _t_ptr(ref_count), _t_ptr(block_table_out),
+                             _t_ptr(ref_count_out), _t_ptr(workspace),
+                             int(workspace.numel() * workspace.element_size()), _t_ptr(status), _stream(stream))
+    _check(rc, "pcp_kv_fork")
+    return block_table_out, ref_count_out
+
+
+def pcp_kv_release(block_table: torch.Tensor, first_page: torch.Tensor, last_page: torch.Tensor,
+                   ref_count: torch.Tensor, block_table_out: Optional[torch.Tensor] = None,
+                   ref_count_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Give back one reference of every block-table entry ``[first_page[r],
+    last_page[r])`` of each row (int32 ``[num_reqs]``); the entries become -1.
+    Returns ``(block_table_out, ref_count_out)``; pass the inputs themselves to
+    work in place."""
+    lib = load()
+    _dev(block_table, "block_table", I32, shape=(-1, -1))
+    dev = block_table.device
+    R, mb = (int(x) for x in block_table.shape)
+    _dev(first_page, "first_page", I32, shape=(R,), device=dev)
+    _dev(last_page, "last_page", I32, shape=(R,), device=dev)
+    _dev(ref_count, "ref_count", I32, shape=(-1,), device=dev)
+    _status(status, dev)
+    nb = int(ref_count.shape[0])
+    block_table_out = _out_like(block_table_out, "block_table_out", (R, mb), dev)
+    ref_count_out = _out_like(ref_count_out, "ref_count_out", (nb,), dev)
+    with _on(dev):
+        rc = lib.pcp_kv_release(_t_ptr(block_table), R, mb, _t_ptr(first_page), _t_ptr(last_page), _t_ptr(ref_count),
+                                nb, _t_ptr(block_table_out), _t_ptr(ref_count_out), _t_ptr(status), _stream(stream))
+    _check(rc, "pcp_kv_release")
+    return block_table_out, ref_count_out
+
+
+def pcp_kv_compact(key_cache: torch.Tensor, value_cache: torch.Tensor, block_table: torch.Tensor,
+                   ref_count: torch.Tensor, block_table_out: Optional[torch.Tensor] = None,
+                   ref_count_out: Optional[torch.Tensor] = None, num_live: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Move the ``n`` live pages to ids ``[0, n)``, in the caches, the counts and the
+    table. Returns ``(block_table_out, ref_count_out, num_live)``, ``num_live``
+    int32 ``[1]`` on the device."""
+    lib = load()
+    dev, nb, bs, slot_bytes = _check_pages(key_cache, value_cache, block_table, ref_count, status)
+    R, mb = (int(x) for x in block_table.shape)
+    block_table_out = _out_like(block_table_out, "block_table_out", (R, mb), dev)
+    ref_count_out = _out_like(ref_count_out, "ref_count_out", (nb,), dev)
+    num_live = _out_like(num_live, "num_live", (1,), dev)
+    workspace = _pages_workspace(workspace, nb, dev)
+    with _on(dev):
+        rc = lib.pcp_kv_compact(_t_ptr(key_cache), _t_ptr(value_cache), nb, bs, slot_bytes, _t_ptr(block_table), R,
+                                mb, _t_ptr(ref_count), _t_ptr(block_table_out), _t_ptr(ref_count_out),
+                                _t_ptr(num_live), _t_ptr(workspace),
+                                int(workspace.numel() * workspace.element_size()), _t_ptr(status), _stream(stream))
+    _check(rc, "pcp_kv_compact")
+    return block_table_out, ref_count_out, num_live
 
 
 def pcp_lse_merge(out_a: torch.Tensor, lse_a: torch.Tensor, out_b: torch.Tensor, lse_b: torch.Tensor,

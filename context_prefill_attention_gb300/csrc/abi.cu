@@ -7,6 +7,7 @@
 
 #include <mutex>
 
+#include "abi_checks.h"
 #include "ctx_table.h"
 #include "pcp.h"
 #include "pcp_internal.h"
@@ -18,28 +19,6 @@ thread_local int g_last_cuda_error = 0;
 // Events recorded around the prefill and decode launches when set (profiling hook).
 thread_local cudaEvent_t g_profile[4] = {nullptr, nullptr, nullptr, nullptr};
 
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// A device buffer as a byte range.
-struct Span {
-    const void* p;
-    size_t n;
-};
-
-// True when two byte ranges share a byte (an empty range shares none).
-inline bool overlap(Span a, Span b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
-}
-
-// True when an output range overlaps any of the ranges in ins[0, n) (kernels
-// read their inputs while other CTAs already write their outputs).
-inline bool overlaps_any(Span out, const Span* ins, int n) {
-    for (int i = 0; i < n; ++i)
-        if (overlap(out, ins[i])) return true;
-    return false;
-}
 }  // namespace
 
 void set_last_cuda_error(cudaError_t e) { g_last_cuda_error = static_cast<int>(e); }
@@ -170,6 +149,7 @@ extern "C" const char* pcp_status_string(int status) {
         case PCP_ERR_CUDA: return "CUDA error";
         case PCP_ERR_TIMEOUT: return "device wait timed out";
         case PCP_ERR_WORKSPACE: return "workspace too small";
+        case PCP_ERR_PAGES: return "no free page";
         default: return "unknown status";
     }
 }
@@ -241,15 +221,9 @@ int pcp::attn_call(const void* q, const void* key_cache, const void* value_cache
               int32_t head_dim, float scale, void* out, float* lse, void* workspace,
               size_t workspace_bytes, int32_t flags, int32_t* status, cudaStream_t s,
               WorkspaceProvider provide) {
-    if (num_rows < 0 || total_q < 0 || num_reqs < 0 || num_q_heads < 1 || num_kv_heads < 1 || max_blocks_per_req < 0 ||
-        num_blocks < 0 || block_size < 1)
-        return PCP_ERR_ARG;
-    if (attn_partials(flags) < 0 || !isfinite(scale)) return PCP_ERR_ARG;
-    if (num_q_heads % num_kv_heads != 0) return PCP_ERR_UNSUPPORTED;
-    if (head_dim != 64 && head_dim != 128) return PCP_ERR_UNSUPPORTED;
-    if (block_size != 8 && block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128)
-        return PCP_ERR_UNSUPPORTED;
-    if (num_q_heads / num_kv_heads > 16) return PCP_ERR_UNSUPPORTED;
+    const int shape = check_attn_shape(num_reqs, max_blocks_per_req, num_blocks, block_size, num_rows, total_q,
+                                       num_q_heads, num_kv_heads, head_dim, scale, attn_partials(flags) >= 0);
+    if (shape != PCP_OK) return shape;
     if (num_rows == 0 || total_q == 0) return PCP_OK;
     if (provide) {
         workspace = nullptr;

@@ -101,7 +101,9 @@ __device__ __forceinline__ void load_row(const uint8_t* slab, int kr, int e0, fl
     }
 }
 
-template <int D, int GMAX, bool F8>
+// RNG (window and shared-prefix calls): the row's own keys (key_range) in splits
+// of a.chunk; a row of one token is a decode row whatever its flag.
+template <int D, int GMAX, bool F8, bool RNG>
 __global__ void __launch_bounds__(kDecThreads)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   PrefillArgs a, float* __restrict__ dec_out, float* __restrict__ dec_lse, int max_splits,
@@ -111,11 +113,14 @@ __global__ void __launch_bounds__(kDecThreads)
     const int split = blockIdx.x, hk = blockIdx.y, ri = blockIdx.z;
     if (!a.row_ok[ri]) return;
     const pcp_row_t row = a.rows[ri];
-    if (!row.is_decode) return;
-    const int32_t C_len = row.kv_end;
-    const int32_t lo = split * kDecodeChunk;
+    if (RNG ? row.q_len != 1 : !row.is_decode) return;
+    KeyRange kr{};
+    if constexpr (RNG) kr = key_range(a, row, a.row_lo[ri]);
+    const int32_t chunk = RNG ? a.chunk : kDecodeChunk;
+    const int32_t C_len = RNG ? kr.len : row.kv_end;  // RNG: slots of the walk, here and below
+    const int32_t lo = split * chunk;
     if (lo >= C_len) return;
-    const int32_t hi = min(C_len, lo + kDecodeChunk);
+    const int32_t hi = min(C_len, lo + chunk);
     const int nslab = (hi - lo + kSlab - 1) / kSlab;
     const int G = a.hq / a.hkv;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -152,7 +157,8 @@ __global__ void __launch_bounds__(kDecThreads)
         const int32_t pg0 = lo / bs;
         const int npages = (hi - 1) / bs - pg0 + 1;
         for (int p = lane; p < npages; p += 32) {
-            const int32_t pg = pg0 + p;
+            int32_t pg = pg0 + p;
+            if (RNG && pg * bs >= kr.sink_slots) pg += kr.shift / bs;
             const int32_t id = pg < a.max_blocks ? __ldg(table + pg) : -1;
             int32_t y = oob;
             if (id >= 0 && id < a.num_blocks) y = id * bs;
@@ -255,7 +261,8 @@ __global__ void __launch_bounds__(kDecThreads)
                     }
                 }
                 const int r_own = base_r + kk_own;
-                const bool live_own = g_own < G && r_own < kSlab && key_base + r_own < hi;
+                const bool live_own = g_own < G && r_own < kSlab && key_base + r_own < hi &&
+                                      (!RNG || kr.live(key_base + r_own));
                 const float s_own = live_own ? v[0] : -INFINITY;
                 // running max of this head over the lanes holding it (lanes dl = g_own mod GP)
                 float mx = s_own;
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(kDecThreads)
                 for (int kk = 0; kk < KPI; ++kk) {
                     const int r = base_r + kk;
                     float vf[VEC];
-                    if (r < kSlab && key_base + r < hi) {
+                    if (r < kSlab && key_base + r < hi && (!RNG || kr.live(key_base + r))) {
                         load_row<VEC, F8>(vslab, r, dl * VEC, vf);
                     } else {
 #pragma unroll
@@ -436,7 +443,61 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-template <int D, int GMAX, bool F8>
+// Merge of a window or shared-prefix call: the results of every row that has more
+// than one partial, by log-sum-exp, into out (bf16) and lse. A row of one token
+// has parts_per_split partials for each split of its own keys; a longer row of
+// a prefix group one for its own keys (partial nparts - 1 of part_out); the rows
+// of a group also those of the prefix's shards (partials 0 .. shards - 1). A
+// longer row outside every group was written by the packed kernel.
+template <int D>
+__global__ void __launch_bounds__(D)
+    range_merge_kernel(PrefillArgs a, const int32_t* __restrict__ row_grp, const int32_t* __restrict__ grp_shards,
+                       const float* __restrict__ dec_out, const float* __restrict__ dec_lse, int max_splits,
+                       int parts_per_split) {
+    const int ri = blockIdx.x, h = blockIdx.y, d = threadIdx.x;
+    if (!a.row_ok[ri]) return;
+    const pcp_row_t row = a.rows[ri];
+    const int32_t grp = row_grp[ri];
+    if (row.q_len > 1 && grp < 0) return;
+    const int shards = grp >= 0 ? grp_shards[grp] : 0;
+    int n = 0;  // partials of the row's own keys in dec_out
+    if (row.q_len == 1) n = parts_per_split * ((key_range(a, row, a.row_lo[ri]).len + a.chunk - 1) / a.chunk);
+    const size_t base = ((size_t)ri * a.hq + h) * (2 * max_splits);
+    const size_t out_stride = (size_t)a.total_q * a.hq * D, lse_stride = (size_t)a.hq * a.total_q;
+    // tokens of a longer row are dealt over gridDim.z
+    for (int32_t t = row.q_start + blockIdx.z; t < row.q_start + row.q_len; t += gridDim.z) {
+        const size_t li = (size_t)h * a.total_q + t, o = ((size_t)t * a.hq + h) * D + d;
+        const bool own = row.q_len > 1;  // partial nparts - 1 holds the own keys
+        float M = own ? a.part_lse[(size_t)(a.nparts - 1) * lse_stride + li] : -INFINITY;
+#pragma unroll 8
+        for (int s = 0; s < n; ++s) M = fmaxf(M, dec_lse[base + s]);
+#pragma unroll 8
+        for (int s = 0; s < shards; ++s) M = fmaxf(M, a.part_lse[(size_t)s * lse_stride + li]);
+        float W = 0.f, O = 0.f;
+        if (M != -INFINITY) {
+            if (own) {
+                W = __expf(a.part_lse[(size_t)(a.nparts - 1) * lse_stride + li] - M);
+                O = W * a.part_out[(size_t)(a.nparts - 1) * out_stride + o];
+            }
+#pragma unroll 8
+            for (int s = 0; s < n; ++s) {
+                const float w = __expf(dec_lse[base + s] - M);
+                W += w;
+                O += w * dec_out[(base + s) * D + d];
+            }
+#pragma unroll 8
+            for (int s = 0; s < shards; ++s) {
+                const float w = __expf(a.part_lse[(size_t)s * lse_stride + li] - M);
+                W += w;
+                O += w * a.part_out[(size_t)s * out_stride + o];
+            }
+        }
+        reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(W > 0.f ? O / W : 0.f);
+        if (d == 0) a.lse[li] = W > 0.f ? M + __logf(W) : -INFINITY;
+    }
+}
+
+template <int D, int GMAX, bool F8, bool RNG>
 int launch_decode_dgf(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                       cudaStream_t stream) {
     const int box_rows = a.block_size < kSlab ? a.block_size : kSlab;
@@ -448,11 +509,11 @@ int launch_decode_dgf(const PrefillArgs& a, float* dec_out, float* dec_lse, int3
     if (!maps) return PCP_ERR_CUDA;
     const int smem = DecCfg<D, GMAX, F8>::kSmem;
     cudaError_t e =
-        cudaFuncSetAttribute(decode_kernel<D, GMAX, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(decode_kernel<D, GMAX, F8, RNG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     dim3 grid(max_splits, a.hkv, a.num_rows);
-    decode_kernel<D, GMAX, F8><<<grid, kDecThreads, smem, stream>>>(tk, tv, a, dec_out, dec_lse, max_splits,
-                                                                    box_rows);
+    decode_kernel<D, GMAX, F8, RNG><<<grid, kDecThreads, smem, stream>>>(tk, tv, a, dec_out, dec_lse, max_splits,
+                                                                         box_rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
@@ -472,8 +533,11 @@ int launch_merge(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t m
 template <int D, int GMAX>
 int launch_decode_dg(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                      cudaStream_t stream) {
-    return a.k_descale ? launch_decode_dgf<D, GMAX, true>(a, dec_out, dec_lse, max_splits, stream)
-                       : launch_decode_dgf<D, GMAX, false>(a, dec_out, dec_lse, max_splits, stream);
+    if (a.chunk > 0)
+        return a.k_descale ? launch_decode_dgf<D, GMAX, true, true>(a, dec_out, dec_lse, max_splits, stream)
+                           : launch_decode_dgf<D, GMAX, false, true>(a, dec_out, dec_lse, max_splits, stream);
+    return a.k_descale ? launch_decode_dgf<D, GMAX, true, false>(a, dec_out, dec_lse, max_splits, stream)
+                       : launch_decode_dgf<D, GMAX, false, false>(a, dec_out, dec_lse, max_splits, stream);
 }
 
 template <int D>
@@ -495,8 +559,11 @@ int launch_decode_d(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_
 
 bool decode_side_applies(const PrefillArgs& a) { return PCP_DECODE_TC && decode_tc_applies(a); }
 
-int launch_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
-                  cudaStream_t stream, int grid) {
+namespace {
+
+// The decode partials of every decode row; *pps: partials per split.
+int launch_decode_parts(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
+                        cudaStream_t stream, int grid, int* parts) {
     if (a.d != 64 && a.d != 128) return PCP_ERR_UNSUPPORTED;
     int rc = PCP_DECODE_TC ? launch_decode_tc(a, dec_out, dec_lse, max_splits, stream, grid) : PCP_ERR_UNSUPPORTED;
     // partials per split: the tensor-core kernel writes one per softmax warpgroup
@@ -507,8 +574,38 @@ int launch_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t 
                        : launch_decode_d<128>(a, dec_out, dec_lse, max_splits, stream);
         pps = 1;
     }
+    *parts = pps;
+    return rc;
+}
+
+}  // namespace
+
+int launch_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
+                  cudaStream_t stream, int grid) {
+    int pps = 1;
+    const int rc = launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, grid, &pps);
     if (rc != PCP_OK) return rc;
     return launch_merge(a, dec_out, dec_lse, max_splits, pps, stream);
+}
+
+int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, int* parts,
+                        cudaStream_t stream) {
+    return launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, 0, parts);
+}
+
+int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32_t* grp_shards,
+                       const float* dec_out, const float* dec_lse, int32_t max_splits, int parts,
+                       cudaStream_t stream) {
+    // longer rows have tokens for several blocks; where no row can be longer than
+    // one token (num_rows == total_q) one block per (row, head) does
+    const dim3 grid(a.num_rows, a.hq, a.total_q > a.num_rows && a.num_prefixes > 0 ? 16 : 1);
+    if (a.d == 64)
+        range_merge_kernel<64><<<grid, 64, 0, stream>>>(a, row_grp, grp_shards, dec_out, dec_lse, max_splits, parts);
+    else
+        range_merge_kernel<128><<<grid, 128, 0, stream>>>(a, row_grp, grp_shards, dec_out, dec_lse, max_splits, parts);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
+    return PCP_OK;
 }
 
 int launch_separate_merge(const PrefillArgs& a, cudaStream_t stream) {

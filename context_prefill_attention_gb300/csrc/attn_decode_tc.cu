@@ -140,6 +140,7 @@ static_assert(TcCfg<true, 4>::kQC % 1024 == 0 && TcCfg<true, 8>::kP % 1024 == 0 
 
 struct DecItem {
     int32_t ri, req, q_start, hk, split, lo, hi, nt;
+    KeyRange kr;  // RNG: lo and hi count slots of this walk
 };
 
 // Item p of the decode work list: first every full kDecodeChunk-key split (row
@@ -148,8 +149,12 @@ struct DecItem {
 // in the order of tail_rows (longest partial first). Dealt in snake order, the
 // CTAs then end within a fraction of a split of each other. The caller's items
 // rise, so the row cursor ri only walks forward over the prefix.
-__device__ __forceinline__ DecItem dec_item(const int32_t* pre, int32_t& ri, int32_t p, const pcp_row_t* rows,
-                                            const int32_t* tail_rows, int32_t num_rows, int32_t hkv) {
+// RNG (window and shared-prefix calls): the row's own keys (key_range) in splits
+// of a.chunk.
+template <bool RNG>
+__device__ __forceinline__ DecItem dec_item(const int32_t* pre, int32_t& ri, int32_t p, const PrefillArgs& a,
+                                            const int32_t* tail_rows) {
+    const int32_t num_rows = a.num_rows, hkv = a.hkv, chunk = RNG ? a.chunk : kDecodeChunk;
     const int32_t nfull = pre[num_rows];
     const bool full = p < nfull;
     int32_t r, rem;
@@ -161,16 +166,18 @@ __device__ __forceinline__ DecItem dec_item(const int32_t* pre, int32_t& ri, int
         rem = p - nfull;
         r = tail_rows[rem / hkv];
     }
-    const pcp_row_t row = rows[r];
-    const int32_t nf = row.kv_end / kDecodeChunk;  // full splits of the row (>= 1 on the full side)
+    const pcp_row_t row = a.rows[r];
     DecItem it;
+    if constexpr (RNG) it.kr = key_range(a, row, a.row_lo[r]);
+    const int32_t len = RNG ? it.kr.len : row.kv_end;
+    const int32_t nf = len / chunk;  // full splits of the row (>= 1 on the full side)
     it.ri = r;
     it.req = row.req;
     it.q_start = row.q_start;
     it.hk = full ? rem / nf : rem % hkv;
     it.split = full ? rem % nf : nf;
-    it.lo = it.split * kDecodeChunk;
-    it.hi = min(row.kv_end, it.lo + kDecodeChunk);
+    it.lo = it.split * chunk;
+    it.hi = min(len, it.lo + chunk);
     it.nt = (it.hi - it.lo + kKeys - 1) / kKeys;
     return it;
 }
@@ -244,7 +251,9 @@ __device__ __forceinline__ float warp_scatter(const float (&x)[GP], int lane) {
 // goes; the eight threads of a row are in one warp and all load before any of
 // them stores. Rows at or past nvalid are written as zeros (their codes may be
 // stale or unwritten cache slots). Run by the 128 converter threads.
-__device__ __forceinline__ void widen_tile(uint8_t* tile, int nvalid, int ct) {
+// live(r): further rows for which it is false are written as zeros too.
+template <typename Live>
+__device__ __forceinline__ void widen_tile(uint8_t* tile, int nvalid, int ct, Live live) {
     constexpr int kHalf = kKeys * 128;
     constexpr int kRpp = kConvThreads / 8;  // rows per pass
     constexpr int kBatch = 4;
@@ -260,7 +269,8 @@ __device__ __forceinline__ void widen_tile(uint8_t* tile, int nvalid, int ct) {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int r = r0 + kRpp * b + rsub;
-            c[b] = r < nvalid ? *reinterpret_cast<const uint4*>(codes + r * kD + 16 * t) : make_uint4(0, 0, 0, 0);
+            c[b] = r < nvalid && live(r) ? *reinterpret_cast<const uint4*>(codes + r * kD + 16 * t)
+                                         : make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
 #pragma unroll
@@ -343,7 +353,8 @@ __device__ __forceinline__ float from16(uint16_t x) {
     return __bfloat162float(__ushort_as_bfloat16(x));
 }
 
-template <bool F8, int GP>
+// RNG: the rows' own key ranges (window and shared-prefix calls).
+template <bool F8, int GP, bool RNG>
 __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, PrefillArgs a, float* __restrict__ dec_out,
@@ -455,7 +466,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         int32_t ri = 0;
         bool ok = true;
         for (int32_t rd = 0, p = item_of_round(0); p < total && ok; p = item_of_round(++rd)) {
-            const DecItem it = dec_item(pre, ri, p, a.rows, tail_rows, a.num_rows, a.hkv);
+            const DecItem it = dec_item<RNG>(pre, ri, p, a, tail_rows);
             // the split's block-table entries as first cache rows; a bad id maps to a
             // row past the cache (zero filled) and reports PCP_ERR_RANGE
             const int32_t* table = a.block_table + (size_t)it.req * a.max_blocks;
@@ -463,7 +474,8 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
             const int npg = (it.hi - it.lo + bs - 1) / bs;
             __syncwarp();
             for (int i = lane; i < npg; i += 32) {
-                const int32_t pg = pg0 + i;
+                int32_t pg = pg0 + i;
+                if (RNG && pg * bs >= it.kr.sink_slots) pg += it.kr.shift / bs;
                 const int32_t id = pg < a.max_blocks ? __ldg(table + pg) : -1;
                 int32_t y = oob;
                 if (id >= 0 && id < a.num_blocks) y = id * bs;
@@ -539,7 +551,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
             bool ok = true;
             const bool s_role = warp == kMmaWarp;
             for (int32_t rd = 0, p = item_of_round(0); p < total && ok; p = item_of_round(++rd)) {
-                const DecItem it = dec_item(pre, ri, p, a.rows, tail_rows, a.num_rows, a.hkv);
+                const DecItem it = dec_item<RNG>(pre, ri, p, a, tail_rows);
                 const int qb = ic & 1;
                 if (s_role && !(ok = mbar_wait(q_full(qb), (ic >> 1) & 1, abort_flag))) break;
                 for (int j = 0; j < it.nt; ++j, ++g) {
@@ -603,7 +615,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         int32_t ri = 0;
         bool ok = true;
         for (int32_t rd = 0, p = item_of_round(0); p < total && ok; p = item_of_round(++rd)) {
-            const DecItem it = dec_item(pre, ri, p, a.rows, tail_rows, a.num_rows, a.hkv);
+            const DecItem it = dec_item<RNG>(pre, ri, p, a, tail_rows);
             const int qb = ic & 1;
             if (cset == 0) {
                 if (!(ok = mbar_wait_warp(qc_full(qb), (ic >> 1) & 1, abort_flag))) break;
@@ -625,7 +637,8 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 const int vs = g % kVS;
                 const int nvalid = min(kKeys, it.hi - it.lo - j * kKeys);
                 if (!(ok = mbar_wait_warp(vc_full(vs), (g / kVS) & 1, abort_flag))) break;
-                widen_tile(smem + C::kV + vs * C::kTileBytes, nvalid, ct);
+                widen_tile(smem + C::kV + vs * C::kTileBytes, nvalid, ct,
+                           [&](int r) { return !RNG || it.kr.live(it.lo + j * kKeys + r); });
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_full(vs));
@@ -648,7 +661,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         bool ok = true;     // every wait of this thread so far completed
         bool stop = false;  // the joint decision to stop (FP8: the warpgroup's; bf16: both's), once per item
         for (int32_t rd = 0, p = item_of_round(0); p < total && !stop; p = item_of_round(++rd), ++ic) {
-            const DecItem it = dec_item(pre, ri, p, a.rows, tail_rows, a.num_rows, a.hkv);
+            const DecItem it = dec_item<RNG>(pre, ri, p, a, tail_rows);
             const float kd = F8 ? __ldg(a.k_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
             const float sl2 = a.scale * kd * kLog2e;
             // FP8: the power of two that undoes each head's q scaling (see q_to_e4m3_terms)
@@ -695,7 +708,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 const uint32_t g = gt + j;
                 if ((int)(g & 1) != wg) continue;
                 const int nvalid = min(kKeys, it.hi - it.lo - j * kKeys);
-                const bool valid = t < nvalid;
+                const bool valid = t < nvalid && (!RNG || it.kr.live(it.lo + j * kKeys + t));
                 ok &= mbar_wait_warp(s_full(g & 1), (g >> 1) & 1, abort_flag);
                 tc_fence_after();
                 uint32_t s[kNS];
@@ -735,7 +748,9 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                     *reinterpret_cast<uint16_t*>(pcol + h * 128 + ((chunk ^ (h & 7)) << 4)) = hi;
                     *reinterpret_cast<uint16_t*>(pcol + (kGS + h) * 128 + ((chunk ^ (h & 7)) << 4)) = lo;
                 }
-                if (!F8 && nvalid < kKeys) {
+                // RNG: also where the tile holds slots between the sinks and the window
+                const bool gaps = RNG && it.lo + j * kKeys < it.kr.lo - it.kr.shift && it.kr.lo - it.kr.shift > it.kr.sinks;
+                if (!F8 && (nvalid < kKeys || gaps)) {
                     // keys past the split's end: zero their V rows (unwritten cache slots in
                     // the last page, stale rows after it) once the tile has landed
                     const uint32_t vs = g % kVS;
@@ -824,7 +839,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
     }
 }
 
-template <bool F8, int GP>
+template <bool F8, int GP, bool RNG>
 int launch_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, cudaStream_t stream,
               int grid) {
     const int64_t slots = a.num_blocks * a.block_size;
@@ -840,10 +855,10 @@ int launch_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_
     if (!maps) return PCP_ERR_CUDA;
     const int smem = TcCfg<F8, GP>::kSmem;
     cudaError_t e =
-        cudaFuncSetAttribute(decode_tc_kernel<F8, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(decode_tc_kernel<F8, GP, RNG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     const int ctas = grid > 0 && grid < num_sms() ? grid : num_sms();
-    decode_tc_kernel<F8, GP><<<ctas, tc_threads(F8, GP), smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
+    decode_tc_kernel<F8, GP, RNG><<<ctas, tc_threads(F8, GP), smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
                                                                               max_splits, q_rows);
     e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
@@ -858,23 +873,34 @@ bool decode_tc_applies(const PrefillArgs& a) {
            a.block_size <= kKeys && kKeys % a.block_size == 0;
 }
 
-int launch_decode_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
-                     cudaStream_t stream, int grid) {
+namespace {
+
+template <bool RNG>
+int launch_tc_any(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, cudaStream_t stream,
+                  int grid) {
     if (!decode_tc_applies(a)) return PCP_ERR_UNSUPPORTED;
     const int G = a.hq / a.hkv;
     // heads per group padded to a power of two (the padded heads' results are not written)
     const int GP = G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : G <= 8 ? 8 : 16;
     if (a.k_descale) {
-        if (GP == 1) return launch_tc<true, 1>(a, dec_out, dec_lse, max_splits, stream, grid);
-        if (GP == 2) return launch_tc<true, 2>(a, dec_out, dec_lse, max_splits, stream, grid);
-        if (GP == 4) return launch_tc<true, 4>(a, dec_out, dec_lse, max_splits, stream, grid);
-        return launch_tc<true, 8>(a, dec_out, dec_lse, max_splits, stream, grid);
+        if (GP == 1) return launch_tc<true, 1, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+        if (GP == 2) return launch_tc<true, 2, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+        if (GP == 4) return launch_tc<true, 4, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+        return launch_tc<true, 8, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
     }
-    if (GP == 1) return launch_tc<false, 1>(a, dec_out, dec_lse, max_splits, stream, grid);
-    if (GP == 2) return launch_tc<false, 2>(a, dec_out, dec_lse, max_splits, stream, grid);
-    if (GP == 4) return launch_tc<false, 4>(a, dec_out, dec_lse, max_splits, stream, grid);
-    if (GP == 8) return launch_tc<false, 8>(a, dec_out, dec_lse, max_splits, stream, grid);
-    return launch_tc<false, 16>(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (GP == 1) return launch_tc<false, 1, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (GP == 2) return launch_tc<false, 2, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (GP == 4) return launch_tc<false, 4, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (GP == 8) return launch_tc<false, 8, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+    return launch_tc<false, 16, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+}
+
+}  // namespace
+
+int launch_decode_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
+                     cudaStream_t stream, int grid) {
+    return a.chunk > 0 ? launch_tc_any<true>(a, dec_out, dec_lse, max_splits, stream, grid)
+                       : launch_tc_any<false>(a, dec_out, dec_lse, max_splits, stream, grid);
 }
 
 }  // namespace pcp

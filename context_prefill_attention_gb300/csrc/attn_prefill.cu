@@ -50,6 +50,8 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "pcp_device.cuh"
 #include "pcp_internal.h"
 
@@ -135,6 +137,7 @@ struct Cfg {
 
 struct Item {
     int32_t req, q_tok0, rows_valid, pos0, k_lo, k_hi, k_end, kb, n_tiles, pass, h0, hk, nslots;
+    int32_t shift;  // packed items: key = slot of the walk + shift past the sink pages
 };
 
 __device__ __forceinline__ int32_t tiles_of(int32_t k_lo, int32_t k_end, int32_t bs) {
@@ -177,6 +180,58 @@ __device__ __forceinline__ Item decode_item(const Unit* units, int32_t idx, int3
     return it;
 }
 
+// Item idx of a packed call (pcp_attn_window, pcp_attn_shared_prefix): a unit's
+// tokens for one kv head. A tile's 128 MMA rows are tpt = 128 / G tokens x the
+// head's G q heads (row r: token r / G, q head r % G), so a row of few tokens
+// fills its tiles, and the keys a tile needs beyond the window are those of tpt
+// tokens, not of 128; the item's head slots are slots consecutive tiles of one
+// row that share the K/V stream. row >= num_rows names prefix group
+// row - num_rows, whose tokens all see exactly the keys [k_lo, k_hi).
+// The keys are walked as whole pages back to back: those of the sinks that lie
+// before the window, then those from the window's first key k_lo on. Slot v of
+// that walk is key v below the sinks' last page end, key v + shift after it.
+// kb holds the number of sink slots, k_end the walk's length, rows_valid tokens.
+__device__ __forceinline__ Item packed_item(const PrefillArgs& a, const Unit& u, int32_t hk, int32_t G) {
+    const int32_t bs = a.block_size, span = a.slots * (kBlockM / G);
+    Item it{};
+    it.nslots = a.slots;
+    it.hk = hk;
+    it.h0 = hk * G;
+    const int32_t mt = u.mt_pass & 0xFFFFFF;
+    it.pass = u.mt_pass >> 24;
+    it.k_hi = u.k_hi;
+    if (u.row >= 0 && u.row < a.num_rows) {
+        const pcp_row_t r = a.rows[u.row];
+        it.req = r.req;
+        it.q_tok0 = r.q_start + mt * span;
+        it.rows_valid = min(span, r.q_len - mt * span);
+        it.pos0 = r.kv_end - r.q_len + mt * span;
+        it.k_lo = max(u.k_lo, it.pos0 - a.window + 1);
+    } else if (u.row >= a.num_rows && u.row - a.num_rows < a.num_prefixes) {
+        const pcp_prefix_t g = a.prefixes[u.row - a.num_rows];
+        it.req = g.req;
+        it.q_tok0 = g.q_start + mt * span;
+        it.rows_valid = min(span, g.q_len - mt * span);
+        it.pos0 = u.k_hi;  // every query lies past the prefix
+        it.k_lo = u.k_lo;
+    } else {
+        return it;  // never written by the scheduler: an empty item
+    }
+    const int32_t sinks = min(a.sinks, it.k_lo);
+    it.kb = (sinks + bs - 1) / bs * bs;
+    it.shift = max(0, it.k_lo / bs * bs - it.kb);
+    it.k_end = min(u.k_hi, it.pos0 + it.rows_valid) - it.shift;
+    it.n_tiles = it.k_end > 0 ? (it.k_end + kBlockN - 1) / kBlockN : 0;
+    return it;
+}
+
+// Whether slot v of a packed item's walk holds a key that some query of the item
+// may see: not past the end, and not between the sinks and the item's first
+// window key (whose cache rows may hold anything).
+__device__ __forceinline__ bool packed_slot_live(const Item& it, int32_t sinks, int32_t v) {
+    return v < it.k_end && (v < sinks || v >= it.k_lo - it.shift);
+}
+
 // One tile of FP8 codes (128 rows x D bytes, row-major) -> bf16 in the
 // 128-byte-swizzled K-major layout of a K or V stage (dims 64h..64h+63 of row
 // r in half h, 16-byte chunk c of that row at chunk c ^ (r & 7)). Run by the 64
@@ -184,8 +239,9 @@ __device__ __forceinline__ Item decode_item(const Unit* units, int32_t idx, int3
 // codes (one 16-byte load) into two 16-byte chunks. In place (D = 128) the codes
 // of row r sit where half 1 of row r goes; the threads of a row are in one warp
 // and all of them load before any of them stores.
-template <int D>
-__device__ __forceinline__ void convert_codes(const uint8_t* codes, uint8_t* dst, int ct) {
+// live(r): rows for which it is false are written as zeros.
+template <int D, typename Live>
+__device__ __forceinline__ void convert_codes(const uint8_t* codes, uint8_t* dst, int ct, Live live) {
     constexpr int kTpr = D / 16;             // threads per row
     constexpr int kRpp = kConvThreads / kTpr;  // rows per pass
     constexpr int kBatch = 4;                // rows per thread between warp barriers
@@ -198,8 +254,10 @@ __device__ __forceinline__ void convert_codes(const uint8_t* codes, uint8_t* dst
     for (int r0 = 0; r0 < kBlockN; r0 += kRpp * kBatch) {
         uint4 c[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
+        for (int b = 0; b < kBatch; ++b) {
             c[b] = *reinterpret_cast<const uint4*>(codes + (r0 + kRpp * b + rsub) * D + 16 * t);
+            if (!live(r0 + kRpp * b + rsub)) c[b] = make_uint4(0, 0, 0, 0);
+        }
         __syncwarp();
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -222,7 +280,9 @@ __device__ __forceinline__ void convert_codes(const uint8_t* codes, uint8_t* dst
 // chunk holds 8 elements whatever the swizzle, so the conversion is
 // elementwise. Values beyond the largest finite f16 saturate to it; the
 // return value says whether any did.
-__device__ __forceinline__ bool convert_q_f16(uint8_t* q_base, int bytes, int ct) {
+// live(row): rows of a 64-dim half tile whose values count for that.
+template <typename Live>
+__device__ __forceinline__ bool convert_q_f16(uint8_t* q_base, int bytes, int ct, Live live) {
     bool over = false;
 #pragma unroll 4
     for (int off = ct * 16; off < bytes; off += kConvThreads * 16) {
@@ -231,7 +291,7 @@ __device__ __forceinline__ bool convert_q_f16(uint8_t* q_base, int bytes, int ct
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float lo = __uint_as_float(e[i] << 16), hi = __uint_as_float(e[i] & 0xFFFF0000u);
-            over |= fabsf(lo) > 65504.f || fabsf(hi) > 65504.f;
+            over |= (fabsf(lo) > 65504.f || fabsf(hi) > 65504.f) && live(off >> 7);
             e[i] = pack_f16x2_satfinite(lo, hi);
         }
         *reinterpret_cast<uint4*>(q_base + off) = w;
@@ -329,7 +389,8 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint6
                (accumulate || ks > 0) ? 1u : 0u);
 }
 
-template <int D, bool F8>
+// PACK: the packed items of the window and shared-prefix calls (packed_item).
+template <int D, bool F8, bool PACK>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, PrefillArgs a) {
@@ -364,8 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int G = a.hq / a.hkv;
-    const bool dual = (G % 2) == 0;
-    const int slots_per_unit = dual ? a.hq / 2 : a.hq;
+    const bool dual = PACK ? a.slots == 2 : (G % 2) == 0;
+    const int slots_per_unit = PACK ? a.hkv : dual ? a.hq / 2 : a.hq;
+    const int tpt = kBlockM / G;  // PACK: tokens of a tile
     const int slots_per_item = dual ? 2 : 1;  // q heads per item (Item::nslots)
     const int32_t bs = a.block_size;
 
@@ -395,6 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_barrier_init();
     }
+    if constexpr (PACK) {
+        // the MMA rows that no token of a tile fills (128 is not a multiple of G): zeros,
+        // which the Q boxes never overwrite, so that these rows' scores stay finite
+        const int used = tpt * G, spare = kBlockM - used;
+        for (int i = threadIdx.x; i < 2 * C::kHalves * spare * 8; i += kThreads)
+            *reinterpret_cast<uint4*>(smem + C::kQ + (i / (spare * 8)) * C::kHalfBytes +
+                                      (used + i / 8 % spare) * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
@@ -414,6 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // per-CTA totals far better than plain round robin, with no atomics.
     auto item_of_round = [&](int32_t r) -> int32_t {
         return r * (int32_t)gridDim.x + ((r & 1) ? (int32_t)(gridDim.x - 1 - blockIdx.x) : (int32_t)blockIdx.x);
+    };
+    auto item_at = [&](int32_t idx) -> Item {
+        if constexpr (PACK) return packed_item(a, a.units[idx / slots_per_unit], idx % slots_per_unit, G);
+        else return decode_item(a.units, idx, slots_per_unit, dual, G, a.rows, a.num_rows, bs);
     };
     // Registers: the launch gives 168 per thread (384 threads); the producer /
     // MMA / converter warpgroup gives back to 104 so the softmax warpgroups can
@@ -437,25 +512,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t round = 0; ok; ++round) {
             const int32_t idx = item_of_round(round);
             if (idx >= total_items) break;
-            const Item it = decode_item(a.units, idx, slots_per_unit, dual, G, a.rows, a.num_rows, bs);
+            const Item it = item_at(idx);
             if (it.n_tiles == 0) continue;
             if (c > 0 && !(ok = mbar_wait_warp(q_empty, (c - 1) & 1, abort_flag))) break;
             if (lane == 0) {
                 const uint32_t qbar = F8 ? qc_full : q_full;
-                mbar_arrive_expect_tx(qbar, it.nslots * C::kTileBytes);
+                mbar_arrive_expect_tx(qbar, PACK ? it.nslots * C::kHalves * tpt * G * 128 : it.nslots * C::kTileBytes);
                 for (int g = 0; g < it.nslots; ++g)
                     for (int h = 0; h < C::kHalves; ++h)
                         tma_load_3d(sbase + C::kQ + g * C::kTileBytes + h * C::kHalfBytes, &tm_q,
-                                    qbar, h * 64, it.h0 + g, it.q_tok0);
+                                    qbar, h * 64, PACK ? it.h0 : it.h0 + g, PACK ? it.q_tok0 + g * tpt : it.q_tok0);
             }
             const int32_t* table = a.block_table + (size_t)it.req * a.max_blocks;
             for (int32_t j = 0; j < it.n_tiles && ok; ++j) {
                 // this lane's page -> first cache row of the page; pages past k_end (and
                 // bad ids) map to a row past the cache, which TMA fills with zeros
                 int32_t y = oob;
-                const int32_t k = it.kb + j * kBlockN + lane * bs;
+                const int32_t k = (PACK ? 0 : it.kb) + j * kBlockN + lane * bs;
                 if (lane < pages && k < it.k_end) {
-                    const int32_t pg = k / bs;
+                    const int32_t pg = (PACK && k >= it.kb ? k + it.shift : k) / bs;
                     const int32_t id = pg < a.max_blocks ? __ldg(table + pg) : -1;
                     if (id >= 0 && id < a.num_blocks) y = id * bs;
                     else report_status(a.status, PCP_ERR_RANGE);
@@ -512,14 +587,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t round = 0; ok; ++round) {
             const int32_t idx = item_of_round(round);
             if (idx >= total_items) break;
-            const Item it = decode_item(a.units, idx, slots_per_unit, dual, G, a.rows, a.num_rows, bs);
+            const Item it = item_at(idx);
             if (it.n_tiles == 0) continue;
             // the item's Q tiles: bf16 -> f16 in place, then ready for the MMAs
             // (D = 128: the softmax threads write each row's e4m3 terms instead)
             if constexpr (!C::kE4) {
                 if (!(ok = mbar_wait_warp(qc_full, cq & 1, abort_flag))) break;
                 ++cq;
-                if (__any_sync(0xffffffffu, convert_q_f16(smem + C::kQ, it.nslots * C::kTileBytes, ct)) && lane == 0)
+                auto q_live = [&](int row) {  // D = 64: a tile is one half of 128 rows
+                    if constexpr (!PACK) return true;
+                    else return row % kBlockM < tpt * G && (row / kBlockM) * tpt + (row % kBlockM) / G < it.rows_valid;
+                };
+                if (__any_sync(0xffffffffu, convert_q_f16(smem + C::kQ, it.nslots * C::kTileBytes, ct, q_live)) &&
+                    lane == 0)
                     report_status(a.status, PCP_ERR_RANGE);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -529,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (!C::kE4) {
                     const int ks = kt % kNK;
                     if (!(ok = mbar_wait_warp(kc_full(ks), (kt / kNK) & 1, abort_flag))) break;
-                    convert_codes<D>(smem + C::code_k(ks), smem + C::kK + ks * C::kTileBytes, ct);
+                    convert_codes<D>(smem + C::code_k(ks), smem + C::kK + ks * C::kTileBytes, ct,
+                                     [](int) { return true; });
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(k_full(ks));
@@ -537,7 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int vs = vt % kNV;
                 if (!(ok = mbar_wait_warp(vc_full(vs), (vt / kNV) & 1, abort_flag))) break;
-                convert_codes<D>(smem + C::code_v(vs), smem + C::kV + vs * C::kTileBytes, ct);
+                convert_codes<D>(smem + C::code_v(vs), smem + C::kV + vs * C::kTileBytes, ct, [&](int row) {
+                    return !PACK || packed_slot_live(it, a.sinks, j * kBlockN + row);
+                });
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_full(vs));
@@ -566,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t round = 0; ok; ++round) {
             const int32_t idx = item_of_round(round);
             if (idx >= total_items) break;
-            const Item it = decode_item(a.units, idx, slots_per_unit, dual, G, a.rows, a.num_rows, bs);
+            const Item it = item_at(idx);
             const int n = it.n_tiles;
             if (n == 0) continue;
             if (!(ok = mbar_wait(q_full, c & 1, abort_flag))) break;
@@ -584,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < n && ok; ++j) {
                 const int vs = vt % kNV;
                 if (!kMerged && !(ok = mbar_wait(v_full(vs), (vt / kNV) & 1, abort_flag))) break;
-                if (j == n - 1 && (it.k_end % bs) != 0) {
+                if (!PACK && j == n - 1 && (it.k_end % bs) != 0) {
                     // Keys at or past k_end inside the last loaded page may never have been
                     // written: zero their V rows so that P = 0 cannot meet a NaN.
                     const int32_t rel = it.k_end - (it.kb + j * kBlockN);
@@ -643,25 +726,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         // on the last tile, Q are free); O done frees the item's last V. Its thread 0
         // arrives, so that the MMA issuer spends no commits on them.
         const bool releaser = g == slots_per_item - 1;
-        uint32_t rel_k = 0, rel_v = 0, cq = 0;
+        uint32_t rel_k = 0, rel_v = 0, cq = 0, vt_all = 0;
         bool ok = true;
         for (int32_t round = 0; ok; ++round) {
             const int32_t idx = item_of_round(round);
             if (idx >= total_items) break;
-            const Item it = decode_item(a.units, idx, slots_per_unit, dual, G, a.rows, a.num_rows, bs);
+            const Item it = item_at(idx);
             const uint32_t my_q = cq;  // Q loads so far (items with key tiles)
             if (it.n_tiles > 0) ++cq;
             if (g >= it.nslots) continue;
-            const int h = it.h0 + g;
+            // PACK: row r is q head r % G of token r / G of the slot's tile
+            const int32_t tl = PACK ? g * tpt + r / G : 0;
+            const int h = PACK ? it.h0 + r % G : it.h0 + g;
             // FP8: the K descale scales every score (the V descale the output, below);
             // it is re-read per tile (an L1 hit) rather than held across the loop,
             // which keeps the score row within the register budget
             const float* kd_ptr = F8 ? a.k_descale + (size_t)it.req * a.hkv + it.hk : nullptr;
-            const bool valid = r < it.rows_valid;
-            const int32_t pos = it.pos0 + min(r, it.rows_valid - 1);
-            const int32_t tok = it.q_tok0 + r;
+            const bool valid = PACK ? r < tpt * G && tl < it.rows_valid : r < it.rows_valid;
+            const int32_t pos = it.pos0 + min(PACK ? tl : r, it.rows_valid - 1);
+            const int32_t tok = it.q_tok0 + (PACK ? tl : r);
             float m = -INFINITY, l = 0.f;
             const int n = it.n_tiles;
+            const uint32_t vt0 = vt_all;  // tiles before this item: V(j) is in stage (vt0 + j) % kNV
+            vt_all += n;
             // FP8, D = 128: once the item's bf16 Q has landed, this thread rewrites its
             // own row as e4m3 terms (the softmax warps are idle until the item's first S)
             // and keeps the row's q scale
@@ -671,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(ok = mbar_wait_warp(qc_full, my_q & 1, abort_flag))) break;
                     bool over = false;
                     qs_row = q_row_to_e4m3(smem + C::kQ + g * C::kTileBytes, r, &over);
-                    if (over) report_status(a.status, PCP_ERR_RANGE);
+                    if (over && (!PACK || valid)) report_status(a.status, PCP_ERR_RANGE);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if ((threadIdx.x & 31) == 0) mbar_arrive(q_full);
@@ -693,23 +780,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t s[128];
                 float* sf = reinterpret_cast<float*>(s);
                 const float sl2 = F8 ? a.scale * __ldg(kd_ptr) * kLog2e * qs_row : a.scale * kLog2e;
-                const int32_t key0 = it.kb + j * kBlockN;
-                const bool full = key0 >= it.k_lo && key0 + kBlockN <= it.k_hi &&
-                                  key0 + kBlockN - 1 <= it.pos0;
-                // S row of this thread into registers, keys outside [k_lo, min(k_hi, pos + 1)) at -inf
+                // PACK: key0 counts slots of the walk less the shift, so that a slot past the
+                // sinks is compared as the key it holds
+                const int32_t key0 = PACK ? j * kBlockN + it.shift : it.kb + j * kBlockN;
+                const bool full = key0 >= (PACK ? max(it.k_lo, it.pos0 + it.rows_valid - a.window) : it.k_lo) &&
+                                  key0 + kBlockN <= it.k_hi && key0 + kBlockN - 1 <= it.pos0;
+                // keys outside [k_lo, min(k_hi, pos + 1)) of the tile's columns [c0, 128) at -inf;
+                // PACK: the row's own window, and the sinks
+                auto mask_scores = [&](float* x, auto c0) {
+                    const int32_t lo = (PACK ? max(it.k_lo, pos - a.window + 1) : it.k_lo) - key0;
+                    const int32_t hi = min(it.k_hi, pos + 1) - key0;
+                    const int32_t sk = PACK ? a.sinks - j * kBlockN : 0;
+#pragma unroll
+                    for (int c2 = decltype(c0)::value; c2 < 128; ++c2)
+                        if ((c2 < lo && (!PACK || c2 >= sk)) || c2 >= hi) x[c2] = -INFINITY;
+                };
+                // S row of this thread into registers, masked
                 auto load_scores = [&]() {
                     tmem_ld32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
                     tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
                     tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
                     tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
                     tmem_wait_ld();
-                    if (!full) {
-                        const int32_t lo = it.k_lo - key0;
-                        const int32_t hi = min(it.k_hi, pos + 1) - key0;
-#pragma unroll
-                        for (int c2 = 0; c2 < 128; ++c2)
-                            if (c2 < lo || c2 >= hi) sf[c2] = -INFINITY;
-                    }
+                    if (!full) mask_scores(sf, std::integral_constant<int, 0>{});
                 };
                 // p of a pair: ex2, or (polynomial knob) the FMA-pipe exp2 for every
                 // kPolyEvery-th pair (a masked key then gets ~1e-38, not 0)
@@ -718,6 +811,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return make_float2(fast_exp2(x.x), fast_exp2(x.y));
                 };
                 load_scores();
+                if constexpr (PACK && !F8) {
+                    // slot 0's threads zero the V rows of slots that no query of the item sees
+                    // (cache rows before the window, unwritten ones past the end) before its
+                    // P, and with it this tile's first PV, is released; S(j) done means that
+                    // V(j) has landed
+                    if (g == 0 && !full && !packed_slot_live(it, a.sinks, j * kBlockN + r)) {
+                        uint8_t* vrow = smem + C::kV + ((vt0 + j) % kNV) * C::kTileBytes + r * 128;
+#pragma unroll
+                        for (int h2 = 0; h2 < C::kHalves; ++h2)
+#pragma unroll
+                            for (int c2 = 0; c2 < 8; ++c2)
+                                *reinterpret_cast<uint4*>(vrow + h2 * C::kHalfBytes + c2 * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
+                }
                 // Fast path: every row of the warp already has a finite reference max m;
                 // p = 2^(s * scale * log2 e - m) straight away, no row max first. With a
                 // bf16 cache, P of keys 0-63 goes to TMEM as soon as it is computed, so
@@ -759,13 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
                         tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
                         tmem_wait_ld();
-                        if (!full) {
-                            const int32_t lo = it.k_lo - key0;
-                            const int32_t hi = min(it.k_hi, pos + 1) - key0;
-#pragma unroll
-                            for (int c2 = 32; c2 < 128; ++c2)
-                                if (c2 < lo || c2 >= hi) sf[c2] = -INFINITY;
-                        }
+                        if (!full) mask_scores(sf, std::integral_constant<int, 32>{});
                     }
                 }
                 if (!exact) continue;
@@ -946,6 +1048,14 @@ __device__ __forceinline__ int32_t block_exclusive_scan(int32_t v, int32_t* warp
     return before;
 }
 
+// The checks every row of a plan has to pass.
+__device__ __forceinline__ bool row_in_range(const pcp_row_t& row, int32_t num_reqs, int32_t total_q, int64_t max_kv) {
+    return row.req >= 0 && row.req < num_reqs && row.q_len >= 1 && row.q_start >= 0 &&
+           (int64_t)row.q_start + row.q_len <= total_q && row.kv_end >= row.q_len && row.kv_end <= max_kv &&
+           row.ctx_len >= 0 && row.ctx_len <= row.kv_end &&
+           (row.is_decode == 0 || (row.is_decode == 1 && row.q_len == 1));
+}
+
 // Key tiles a unit's item walks (its cost in the schedule).
 __device__ __forceinline__ int32_t unit_cost(const Unit& u, const pcp_row_t* rows, int32_t bs) {
     const pcp_row_t row = rows[u.row];
@@ -957,6 +1067,73 @@ __device__ __forceinline__ int32_t unit_cost(const Unit& u, const pcp_row_t* row
 
 // Partial last splits of decode rows, bucketed by their 128-key tiles (1 .. 16).
 constexpr int kTailBuckets = kDecodeChunk / kBlockN;
+
+// units[0, n) into sorted by descending cost (key tiles), by the whole block;
+// keys: kSortCap entries of shared memory.
+template <typename Cost>
+__device__ __forceinline__ void sort_units(const Unit* units, Unit* sorted, int32_t n, unsigned long long* keys,
+                                           int32_t* warp_sums, Cost cost_of) {
+    if (n > kSortCap) {
+        // Counting sort, longest first: class c = kCostBuckets - 1 - min(cost,
+        // kCostBuckets - 1); count, exclusive scan, scatter. Units of one class
+        // land in any order (every item writes only its own outputs, so the
+        // order changes no result).
+        int32_t* cnt = reinterpret_cast<int32_t*>(keys);
+        for (int32_t i = threadIdx.x; i < kCostBuckets; i += kSchedThreads) cnt[i] = 0;
+        __syncthreads();
+        for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
+            const int32_t c = kCostBuckets - 1 - min(cost_of(units[i]), kCostBuckets - 1);
+            atomicAdd(&cnt[c], 1);
+        }
+        __syncthreads();
+        constexpr int kPer = kCostBuckets / kSchedThreads;  // consecutive classes per thread
+        int32_t local[kPer], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            local[k] = cnt[threadIdx.x * kPer + k];
+            sum += local[k];
+        }
+        int32_t tot;
+        int32_t run = block_exclusive_scan(sum, warp_sums, &tot);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            cnt[threadIdx.x * kPer + k] = run;
+            run += local[k];
+        }
+        __syncthreads();
+        for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
+            const Unit u = units[i];
+            const int32_t c = kCostBuckets - 1 - min(cost_of(u), kCostBuckets - 1);
+            sorted[atomicAdd(&cnt[c], 1)] = u;
+        }
+        return;
+    }
+    int32_t pow2 = 1;
+    while (pow2 < n) pow2 <<= 1;
+    for (int32_t i = threadIdx.x; i < pow2; i += kSchedThreads) {
+        unsigned long long key = ~0ull;
+        if (i < n) {
+            const int32_t cost = cost_of(units[i]);
+            key = ((unsigned long long)(0x7FFFFFFF - cost) << 32) | (unsigned)i;
+        }
+        keys[i] = key;
+    }
+    __syncthreads();
+    for (int32_t k = 2; k <= pow2; k <<= 1) {
+        for (int32_t jj = k >> 1; jj > 0; jj >>= 1) {
+            for (int32_t i = threadIdx.x; i < pow2; i += kSchedThreads) {
+                const int32_t l = i ^ jj;
+                if (l > i) {
+                    const unsigned long long x = keys[i], y = keys[l];
+                    const bool up = (i & k) == 0;
+                    if ((x > y) == up) { keys[i] = y; keys[l] = x; }
+                }
+            }
+            __syncthreads();
+        }
+    }
+    for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) sorted[i] = units[(int32_t)(keys[i] & 0xFFFFFFFFu)];
+}
 
 // Check every row, then build the prefill work list: one unit per (valid
 // non-decode row, 128-token tile, pass), ordered by the number of key tiles,
@@ -993,10 +1170,7 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         int32_t cnt = 0, dcnt = 0;
         if (ri < num_rows) {
             row = rows[ri];
-            const bool ok = row.req >= 0 && row.req < a.num_reqs && row.q_len >= 1 && row.q_start >= 0 &&
-                            (int64_t)row.q_start + row.q_len <= a.total_q && row.kv_end >= row.q_len &&
-                            row.kv_end <= max_kv && row.ctx_len >= 0 && row.ctx_len <= row.kv_end &&
-                            (row.is_decode == 0 || (row.is_decode == 1 && row.q_len == 1));
+            const bool ok = row_in_range(row, a.num_reqs, a.total_q, max_kv);
             row_ok[ri] = ok ? 1 : 0;
             if (!ok) report_status(a.status, PCP_ERR_RANGE);
             if (ok && !row.is_decode) cnt = ((row.q_len + kBlockM - 1) / kBlockM) * passes;
@@ -1058,66 +1232,148 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
     }
     // every thread's units[] writes must be visible before any thread reads them
     __syncthreads();
-    if (n > kSortCap) {
-        // Counting sort, longest first: class c = kCostBuckets - 1 - min(cost,
-        // kCostBuckets - 1); count, exclusive scan, scatter. Units of one class
-        // land in any order (every item writes only its own outputs, so the
-        // order changes no result).
-        int32_t* cnt = reinterpret_cast<int32_t*>(keys);
-        for (int32_t i = threadIdx.x; i < kCostBuckets; i += kSchedThreads) cnt[i] = 0;
-        __syncthreads();
-        for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
-            const int32_t c = kCostBuckets - 1 - min(unit_cost(units[i], rows, bs), kCostBuckets - 1);
-            atomicAdd(&cnt[c], 1);
-        }
-        __syncthreads();
-        constexpr int kPer = kCostBuckets / kSchedThreads;  // consecutive classes per thread
-        int32_t local[kPer], sum = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            local[k] = cnt[threadIdx.x * kPer + k];
-            sum += local[k];
-        }
-        int32_t tot;
-        int32_t run = block_exclusive_scan(sum, warp_sums, &tot);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            cnt[threadIdx.x * kPer + k] = run;
-            run += local[k];
-        }
-        __syncthreads();
-        for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
-            const Unit u = units[i];
-            const int32_t c = kCostBuckets - 1 - min(unit_cost(u, rows, bs), kCostBuckets - 1);
-            sorted[atomicAdd(&cnt[c], 1)] = u;
-        }
-        return;
+    sort_units(units, sorted, n, keys, warp_sums, [&](const Unit& u) { return unit_cost(u, rows, bs); });
+}
+
+// The scheduler of the window and shared-prefix calls: the row checks, the
+// packed work list (packed_item; longest first) and the decode work items, as
+// schedule_kernel lays them out but over each row's own keys and in splits of
+// a.chunk keys. A row of one token is a decode row whatever its flag. Window
+// calls (no prefixes): one unit per a.slots tiles of a longer row. Shared-prefix
+// calls: a group's units, per a.slots tiles of its tokens and shard of its
+// prefix (a.nparts - 1 shards of whole pages at most), write partials 1 ..
+// nparts - 1, a longer row's own keys partial nparts; a row outside every
+// group attends all its keys into the result at once. row_lo: each row's first
+// own key; row_grp: its group or -1; grp_shards: each group's shards (0: bad).
+__global__ void __launch_bounds__(kSchedThreads, 1)
+    range_schedule_kernel(PrefillArgs a, Unit* units, Unit* sorted, int32_t* header, int32_t* row_ok,
+                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
+                          int64_t max_units) {
+    __shared__ int32_t warp_sums[32];
+    __shared__ int32_t tail_cnt[kTailBuckets + 1], tail_off[kTailBuckets + 1], tail_fill[kTailBuckets + 1];
+    __shared__ __align__(16) unsigned long long keys[kSortCap];
+    if (threadIdx.x <= kTailBuckets) {
+        tail_cnt[threadIdx.x] = 0;
+        tail_fill[threadIdx.x] = 0;
     }
-    int32_t pow2 = 1;
-    while (pow2 < n) pow2 <<= 1;
-    for (int32_t i = threadIdx.x; i < pow2; i += kSchedThreads) {
-        unsigned long long key = ~0ull;
-        if (i < n) {
-            const int32_t cost = unit_cost(units[i], rows, bs);
-            key = ((unsigned long long)(0x7FFFFFFF - cost) << 32) | (unsigned)i;
+    const int32_t num_rows = a.num_rows, bs = a.block_size, ng = a.num_prefixes;
+    const int32_t span = a.slots * (kBlockM / (a.hq / a.hkv));
+    const int64_t max_kv = (int64_t)a.max_blocks * bs;
+    // groups: fields in range, and the tokens after those of every earlier group
+    for (int32_t g = threadIdx.x; g < ng; g += kSchedThreads) {
+        const pcp_prefix_t p = a.prefixes[g];
+        bool ok = p.q_start >= 0 && p.q_len >= 1 && (int64_t)p.q_start + p.q_len <= a.total_q && p.req >= 0 &&
+                  p.req < a.num_reqs && p.prefix_len >= 1 && p.prefix_len <= max_kv;
+        for (int32_t e = 0; e < g && ok; ++e) {
+            const pcp_prefix_t o = a.prefixes[e];
+            ok = (int64_t)p.q_start >= (int64_t)o.q_start + o.q_len;
         }
-        keys[i] = key;
+        if (!ok) report_status(a.status, PCP_ERR_RANGE);
+        grp_shards[g] = ok ? min(a.nparts - 1, (p.prefix_len + kBlockN - 1) / kBlockN) : 0;
     }
     __syncthreads();
-    for (int32_t k = 2; k <= pow2; k <<= 1) {
-        for (int32_t jj = k >> 1; jj > 0; jj >>= 1) {
-            for (int32_t i = threadIdx.x; i < pow2; i += kSchedThreads) {
-                const int32_t l = i ^ jj;
-                if (l > i) {
-                    const unsigned long long x = keys[i], y = keys[l];
-                    const bool up = (i & k) == 0;
-                    if ((x > y) == up) { keys[i] = y; keys[l] = x; }
-                }
+    int32_t base = 0, dbase = 0;
+    for (int32_t r0 = 0; r0 < num_rows; r0 += kSchedThreads) {
+        const int32_t ri = r0 + threadIdx.x;
+        pcp_row_t row{};
+        int32_t cnt = 0, dcnt = 0, lo = 0, grp = -1;
+        if (ri < num_rows) {
+            row = a.rows[ri];
+            // (without prefixes the packed kernel is not launched for num_rows >= total_q)
+            bool ok = row_in_range(row, a.num_reqs, a.total_q, max_kv) &&
+                      (row.q_len == 1 || ng > 0 || a.total_q > num_rows);
+            for (int32_t g = 0; g < ng && ok; ++g) {
+                const pcp_prefix_t p = a.prefixes[g];
+                const int64_t p1 = (int64_t)p.q_start + p.q_len, r1 = (int64_t)row.q_start + row.q_len;
+                if (r1 <= p.q_start || row.q_start >= p1) continue;
+                // the row's tokens lie inside the group, past the prefix
+                ok = grp_shards[g] > 0 && row.q_start >= p.q_start && r1 <= p1 &&
+                     row.kv_end - row.q_len >= p.prefix_len;
+                grp = g;
+                lo = p.prefix_len;
             }
-            __syncthreads();
+            if (!ok) {
+                report_status(a.status, PCP_ERR_RANGE);
+                lo = 0;
+                grp = -1;
+            }
+            row_ok[ri] = ok ? 1 : 0;
+            row_lo[ri] = lo;
+            row_grp[ri] = grp;
+            if (ok && row.q_len > 1) cnt = (row.q_len + span - 1) / span;
+            if (ok && row.q_len == 1) {
+                const int32_t nv = key_range(a, row, lo).len;
+                dcnt = (nv / a.chunk) * a.hkv;
+                const int32_t part = nv % a.chunk;
+                if (part) atomicAdd(&tail_cnt[(part + kBlockN - 1) / kBlockN], 1);
+            }
         }
+        int32_t dtot;
+        const int32_t doff = dbase + block_exclusive_scan(dcnt, warp_sums, &dtot);
+        if (ri < num_rows) dec_pre[ri] = doff;
+        dbase += dtot;
+        int32_t tot;
+        const int32_t off = base + block_exclusive_scan(cnt, warp_sums, &tot);
+        for (int32_t u = 0; u < cnt; ++u) {
+            if (off + u >= max_units) break;
+            Unit x;
+            x.row = ri;
+            x.mt_pass = u | ((grp >= 0 ? a.nparts : 0) << 24);
+            x.k_lo = lo;
+            x.k_hi = row.kv_end;
+            units[off + u] = x;
+        }
+        base += tot;
     }
-    for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) sorted[i] = units[(int32_t)(keys[i] & 0xFFFFFFFFu)];
+    for (int32_t g0 = 0; g0 < ng; g0 += kSchedThreads) {
+        const int32_t g = g0 + threadIdx.x;
+        int32_t cnt = 0, shards = 0;
+        pcp_prefix_t p{};
+        if (g < ng) {
+            p = a.prefixes[g];
+            shards = grp_shards[g];
+            cnt = shards * ((p.q_len + span - 1) / span);
+        }
+        int32_t tot;
+        const int32_t off = base + block_exclusive_scan(cnt, warp_sums, &tot);
+        const int32_t pages = (p.prefix_len + bs - 1) / bs;
+        for (int32_t u = 0; u < cnt; ++u) {
+            if (off + u >= max_units) break;
+            const int32_t sh = u % shards;
+            Unit x;
+            x.row = num_rows + g;
+            x.mt_pass = (u / shards) | ((1 + sh) << 24);
+            x.k_lo = (int32_t)((int64_t)pages * sh / shards) * bs;
+            x.k_hi = min(p.prefix_len, (int32_t)((int64_t)pages * (sh + 1) / shards) * bs);
+            units[off + u] = x;
+        }
+        base += tot;
+    }
+    const int32_t n = (int32_t)min((int64_t)base, max_units);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int32_t t = 0;
+        for (int b = kTailBuckets; b >= 1; --b) {
+            tail_off[b] = t;
+            t += tail_cnt[b];
+        }
+        header[0] = n;
+        header[1] = dbase + t * a.hkv;
+        dec_pre[num_rows] = dbase;
+    }
+    __syncthreads();
+    for (int32_t ri = threadIdx.x; ri < num_rows; ri += kSchedThreads) {
+        if (!row_ok[ri]) continue;
+        const pcp_row_t row = a.rows[ri];
+        if (row.q_len != 1) continue;
+        const int32_t part = key_range(a, row, row_lo[ri]).len % a.chunk;
+        if (!part) continue;
+        const int b = (part + kBlockN - 1) / kBlockN;
+        dec_pre[num_rows + 1 + tail_off[b] + atomicAdd(&tail_fill[b], 1)] = ri;
+    }
+    __syncthreads();
+    const int32_t G = a.hq / a.hkv;
+    sort_units(units, sorted, n, keys, warp_sums, [&](const Unit& u) { return packed_item(a, u, 0, G).n_tiles; });
 }
 
 // ---------------------------------------------------------------- tensor maps
@@ -1165,7 +1421,7 @@ bool make_row_map(CUtensorMap* m, const void* base, int D, int esize, int64_t mi
     return r == CUDA_SUCCESS;
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool PACK>
 int launch_prefill_d(const PrefillArgs& a, cudaStream_t stream, int grid) {
     CUtensorMap tq, tk, tv;
     const int64_t slots = a.num_blocks * a.block_size;
@@ -1175,18 +1431,32 @@ int launch_prefill_d(const PrefillArgs& a, cudaStream_t stream, int grid) {
                                make_row_map(&tv, a.value_cache, D, 1, a.hkv, slots, a.block_size)
                          : make_map(&tk, a.key_cache, D, a.hkv, slots, a.block_size) &&
                                make_map(&tv, a.value_cache, D, a.hkv, slots, a.block_size);
-    if (!maps || !make_map(&tq, a.q, D, a.hq, a.total_q, kBlockM)) return PCP_ERR_CUDA;
+    // PACK: a Q box is the G heads of one kv head for 128 / G tokens, token-major rows
+    const int G = a.hq / a.hkv;
+    const bool q_map = PACK ? make_box_map(&tq, a.q, D, 2, a.hq, a.total_q, 64, G, kBlockM / G, true)
+                            : make_map(&tq, a.q, D, a.hq, a.total_q, kBlockM);
+    if (!maps || !q_map) return PCP_ERR_CUDA;
     const int smem = Cfg<D, F8>::kSmem;
-    cudaError_t e =
-        cudaFuncSetAttribute(prefill_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, F8, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     // persistent: the work list is dealt over however many CTAs run (fewer when
     // the decode rows take some SMs beside it)
     const int ctas = grid > 0 && grid < num_sms() ? grid : num_sms();
-    prefill_kernel<D, F8><<<ctas, kThreads, smem, stream>>>(tq, tk, tv, a);
+    prefill_kernel<D, F8, PACK><<<ctas, kThreads, smem, stream>>>(tq, tk, tv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
+}
+
+template <bool PACK>
+int launch_prefill_any(const PrefillArgs& a, cudaStream_t stream, int grid) {
+    const bool f8 = a.k_descale != nullptr;
+    if (a.d == 64)
+        return f8 ? launch_prefill_d<64, true, PACK>(a, stream, grid) : launch_prefill_d<64, false, PACK>(a, stream, grid);
+    if (a.d == 128)
+        return f8 ? launch_prefill_d<128, true, PACK>(a, stream, grid)
+                  : launch_prefill_d<128, false, PACK>(a, stream, grid);
+    return PCP_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -1201,14 +1471,21 @@ int launch_schedule(const PrefillArgs& a, int32_t flags, Unit* units, Unit* unit
     return PCP_OK;
 }
 
-int launch_prefill(const PrefillArgs& a, cudaStream_t stream, int grid) {
-    const bool f8 = a.k_descale != nullptr;
-    if (a.d == 64)
-        return f8 ? launch_prefill_d<64, true>(a, stream, grid) : launch_prefill_d<64, false>(a, stream, grid);
-    if (a.d == 128)
-        return f8 ? launch_prefill_d<128, true>(a, stream, grid) : launch_prefill_d<128, false>(a, stream, grid);
-    return PCP_ERR_UNSUPPORTED;
+int launch_range_schedule(const PrefillArgs& a, Unit* units, Unit* units_sorted, int32_t* header, int32_t* row_ok,
+                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
+                          int64_t max_units, cudaStream_t stream) {
+    range_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(a, units, units_sorted, header, row_ok, row_lo, row_grp,
+                                                           grp_shards, dec_pre, max_units);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
+    return PCP_OK;
 }
+
+int launch_prefill(const PrefillArgs& a, cudaStream_t stream, int grid) {
+    return launch_prefill_any<false>(a, stream, grid);
+}
+
+int launch_packed(const PrefillArgs& a, cudaStream_t stream) { return launch_prefill_any<true>(a, stream, 0); }
 
 bool make_kv_row_map(CUtensorMap* m, const void* base, int D, int esize, int64_t mid, int64_t outer, int rows) {
     return make_row_map(m, base, D, esize, mid, outer, rows);

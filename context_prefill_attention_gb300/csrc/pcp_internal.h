@@ -100,7 +100,38 @@ struct PrefillArgs {
     // null for a bf16 cache
     const float* k_descale;
     const float* v_descale;
+    // Window and shared-prefix calls (pcp_attn_window, pcp_attn_shared_prefix);
+    // chunk is 0 in the others, which read none of these.
+    int32_t chunk;              // keys per decode split, a multiple of 128, at most kDecodeChunk
+    int32_t window, sinks;      // keys a query sees: the last `window` ones and the first `sinks`
+    int32_t slots;              // token tiles per packed item: 1 or 2
+    const int32_t* row_lo;      // first own key of each row (0, or its group's prefix length)
+    const pcp_prefix_t* prefixes;
+    int32_t num_prefixes;
 };
+
+#ifdef __CUDACC__
+// The keys of a one-token row in a window or shared-prefix call, walked as whole
+// pages back to back: the pages of the sinks that lie before the window, then
+// those from the first window key on. Slot v of the walk is key v below
+// sink_slots and key v + shift from there on; slots [sinks, lo - shift) hold
+// keys that the row does not see.
+struct KeyRange {
+    int32_t lo, sinks, sink_slots, shift, len;
+    __device__ __forceinline__ bool live(int32_t v) const { return v < sinks || v >= lo - shift; }
+};
+
+__device__ __forceinline__ KeyRange key_range(const PrefillArgs& a, const pcp_row_t& row, int32_t row_lo) {
+    KeyRange k;
+    const int32_t bs = a.block_size;
+    k.lo = max(row_lo, row.kv_end - a.window);
+    k.sinks = min(a.sinks, k.lo);
+    k.sink_slots = (k.sinks + bs - 1) / bs * bs;
+    k.shift = max(0, k.lo / bs * bs - k.sink_slots);
+    k.len = row.kv_end - k.shift;
+    return k;
+}
+#endif
 
 // TMA map of a cache viewed as [outer][mid][D] elements of esize bytes (1: FP8
 // codes, 2: bf16) with a box of D x 1 x rows, no swizzle.
@@ -149,6 +180,17 @@ int launch_decode_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32
 // persistent kernel that PCP_ATTN_DECODE_SMS confines to a few SMs).
 bool decode_side_applies(const PrefillArgs& a);
 int launch_separate_merge(const PrefillArgs& a, cudaStream_t stream);
+// Window and shared-prefix calls: the schedule, the packed kernel over its work
+// list, the decode partials (*parts: partials per split) and their merge.
+int launch_range_schedule(const PrefillArgs& a, Unit* units, Unit* units_sorted, int32_t* header, int32_t* row_ok,
+                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
+                          int64_t max_units, cudaStream_t stream);
+int launch_packed(const PrefillArgs& a, cudaStream_t stream);
+int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, int* parts,
+                        cudaStream_t stream);
+int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32_t* grp_shards,
+                       const float* dec_out, const float* dec_lse, int32_t max_splits, int parts,
+                       cudaStream_t stream);
 int launch_cache_write(const void* k, const void* v, const int64_t* slot, int32_t num_tokens,
                        int32_t vec_per_tok, void* key_cache, void* value_cache, int64_t num_slots,
                        int32_t* status, cudaStream_t stream);

@@ -6,6 +6,7 @@
 // a row's seq_len is its end position). Contiguous per-rank slices:
 // "Feat/pcp qwen36 hybrid", "Changes". Slot mapping and PAD masking: commit
 // "drop pcp_has_prefill" on the row-plan page.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <vector>
@@ -168,4 +169,64 @@ extern "C" int32_t pcp_decode_sms(const pcp_row_t* rows, int32_t num_rows, int32
     if (k < 1) k = 1;
     if (2 * k >= num_sms) return 0;  // decode-heavy: HBM, not the SM count, bounds it
     return k;
+}
+
+extern "C" int pcp_build_prefix_groups(const pcp_row_t* rows, int32_t num_rows, const int32_t* block_table,
+                                       int32_t num_reqs, int32_t max_blocks_per_req, int32_t block_size,
+                                       int32_t min_prefix_len, pcp_prefix_t* prefixes, int32_t capacity,
+                                       int32_t* num_prefixes) {
+    constexpr int32_t kMaxGroups = 1024;  // pcp_attn_shared_prefix takes no more
+    if (num_rows < 0 || num_reqs < 0 || max_blocks_per_req < 0 || block_size < 1 || min_prefix_len < 1 ||
+        capacity < 0 || !num_prefixes || (num_rows > 0 && (!rows || !block_table)) || (capacity > 0 && !prefixes))
+        return PCP_ERR_ARG;
+    *num_prefixes = 0;
+    try {
+        std::vector<int32_t> order(num_rows);
+        for (int32_t i = 0; i < num_rows; ++i) {
+            order[i] = i;
+            const pcp_row_t& r = rows[i];
+            if (r.req < 0 || r.req >= num_reqs || r.q_start < 0 || r.q_len < 1 || r.kv_end < r.q_len ||
+                (int64_t)r.q_start + r.q_len > INT32_MAX || r.kv_end > (int64_t)max_blocks_per_req * block_size)
+                return PCP_ERR_RANGE;
+        }
+        std::stable_sort(order.begin(), order.end(),
+                         [&](int32_t a, int32_t b) { return rows[a].q_start < rows[b].q_start; });
+        int32_t out = 0;
+        int32_t lead = -1, members = 0;  // the group so far: its first row, its rows, ...
+        int64_t pages = 0, end = 0;      // ... the pages they share, where its tokens end
+        auto close = [&]() {
+            if (members >= 2 && out < kMaxGroups) {
+                if (out >= capacity) return false;
+                const pcp_row_t& r = rows[lead];
+                prefixes[out++] = {r.q_start, (int32_t)(end - r.q_start), r.req, (int32_t)(pages * block_size)};
+            }
+            return true;
+        };
+        for (int32_t i : order) {
+            const pcp_row_t& r = rows[i];
+            const int64_t own = (r.kv_end - r.q_len) / block_size;  // whole pages before the row's first token
+            int64_t common = 0;
+            if (lead >= 0 && r.q_start == end) {
+                const int32_t* a = block_table + (size_t)rows[lead].req * max_blocks_per_req;
+                const int32_t* b = block_table + (size_t)r.req * max_blocks_per_req;
+                const int64_t most = pages < own ? pages : own;
+                while (common < most && a[common] == b[common] && a[common] >= 0) ++common;
+            }
+            if (common * block_size >= min_prefix_len && members * common >= (members - 1) * pages) {
+                pages = common;
+                ++members;
+            } else {
+                if (!close()) return PCP_ERR_RANGE;
+                lead = i;
+                members = 1;
+                pages = own;
+            }
+            end = (int64_t)r.q_start + r.q_len;
+        }
+        if (!close()) return PCP_ERR_RANGE;
+        *num_prefixes = out;
+        return PCP_OK;
+    } catch (...) {  // no memory for the order
+        return PCP_ERR_ARG;
+    }
 }

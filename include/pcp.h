@@ -68,6 +68,7 @@ typedef struct CUstream_st* pcp_stream_t; /* == cudaStream_t */
 #define PCP_ERR_CUDA (-5)        /* a CUDA call failed; see pcp_last_cuda_error() */
 #define PCP_ERR_TIMEOUT (-6)     /* a bounded device wait ran out (reported via status) */
 #define PCP_ERR_WORKSPACE (-7)   /* workspace missing or too small */
+#define PCP_ERR_PAGES (-8)       /* no free page left in the cache (reported via status) */
 
 /* split modes of pcp_build_row_plan */
 #define PCP_SPLIT_CONTIGUOUS 0
@@ -110,6 +111,13 @@ typedef struct CUstream_st* pcp_stream_t; /* == cudaStream_t */
 typedef struct pcp_row_t {
     int32_t req, shard, q_start, q_len, ctx_len, kv_end, causal_off, is_decode;
 } pcp_row_t;
+
+/* Tokens that share a prefix (pcp_attn_shared_prefix): every token of the packed
+ * range [q_start, q_start + q_len) has the same keys at positions
+ * [0, prefix_len), which request req's block-table row names. All int32. */
+typedef struct pcp_prefix_t {
+    int32_t q_start, q_len, req, prefix_len;
+} pcp_prefix_t;
 
 /*
  * pcp_build_row_plan — host function, pure and deterministic.
@@ -340,6 +348,165 @@ int pcp_attn_varlen_fp8kv(const void* q, const void* key_cache, const void* valu
                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
                           void* out, float* lse, void* workspace, size_t workspace_bytes, int32_t flags,
                           int32_t* status, pcp_stream_t stream);
+
+/*
+ * pcp_attn_window — device. No counterpart on the pages: pcp_attn_varlen for
+ * layers whose queries see a sliding window and a few first tokens. The query at
+ * position p attends the keys k <= p with k > p - window or k < num_sinks
+ * (window >= 1 counts the query's own position; num_sinks >= 0): prompt, cached-prefix and decode rows in one
+ * call, out and lse as there. Only pages that hold such a key are read: pages
+ * wholly between the sinks and a row's window may be released (their
+ * block-table entries are not looked at), and within the pages read the rows of
+ * keys that no query of the work item sees may hold anything.
+ * A row of one token takes the decode path whatever its is_decode. The rows'
+ * tokens are disjoint, so a call with num_rows >= total_q has one-token rows
+ * only: any longer row in it is refused (skipped, *status = PCP_ERR_RANGE).
+ * Every other argument, limit, check and error is that of pcp_attn_varlen;
+ * there are no flags. workspace: at least pcp_attn_window_workspace_size(
+ * num_rows, total_q, Hq, Hkv, D, max_blocks_per_req * block_size, block_size,
+ * window, num_sinks) bytes. Errors: PCP_ERR_ARG also for window < 1 or
+ * num_sinks < 0.
+ * pcp_attn_window_fp8kv: the same over an FP8 (e4m3) cache, with the descales
+ * and numerics of pcp_attn_varlen_fp8kv.
+ */
+size_t pcp_attn_window_workspace_size(int32_t num_rows, int32_t total_q, int32_t num_q_heads,
+                                      int32_t num_kv_heads, int32_t head_dim, int32_t max_kv_len,
+                                      int32_t block_size, int32_t window, int32_t num_sinks);
+int pcp_attn_window(const void* q, const void* key_cache, const void* value_cache,
+                    const int32_t* block_table, int32_t num_reqs, int32_t max_blocks_per_req,
+                    int64_t num_blocks, int32_t block_size, const pcp_row_t* rows, int32_t num_rows,
+                    int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                    float scale, int32_t window, int32_t num_sinks, void* out, float* lse, void* workspace,
+                    size_t workspace_bytes, int32_t* status, pcp_stream_t stream);
+int pcp_attn_window_fp8kv(const void* q, const void* key_cache, const void* value_cache,
+                          const float* k_descale, const float* v_descale, const int32_t* block_table,
+                          int32_t num_reqs, int32_t max_blocks_per_req, int64_t num_blocks,
+                          int32_t block_size, const pcp_row_t* rows, int32_t num_rows, int32_t total_q,
+                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                          int32_t window, int32_t num_sinks, void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, int32_t* status, pcp_stream_t stream);
+
+/*
+ * pcp_build_prefix_groups — host function, pure. The prefix groups of a row plan
+ * for pcp_attn_shared_prefix, from the block tables: rows whose tokens follow
+ * each other and whose tables begin with the same pages. rows[num_rows] and
+ * block_table[num_reqs][max_blocks_per_req] in host memory. The rows are walked
+ * by q_start; a row joins the group before it when its tokens continue the
+ * group's, both share at least min_prefix_len keys of whole pages (before the
+ * first new token of every row), and joining does not lower the pages that the
+ * group saves ((rows - 1) x shared pages). Groups of one row are dropped; at
+ * most 1024 groups are written (later ones are dropped: their rows attend all
+ * their keys themselves, with the same result).
+ * Outputs: prefixes[capacity] (num_rows / 2 always suffice) and *num_prefixes.
+ * Errors: PCP_ERR_ARG (null pointer, negative size, min_prefix_len or
+ * block_size < 1), PCP_ERR_RANGE (a row's request outside [0, num_reqs) or its
+ * keys beyond max_blocks_per_req pages; more groups than capacity).
+ */
+int pcp_build_prefix_groups(const pcp_row_t* rows, int32_t num_rows, const int32_t* block_table,
+                            int32_t num_reqs, int32_t max_blocks_per_req, int32_t block_size,
+                            int32_t min_prefix_len, pcp_prefix_t* prefixes, int32_t capacity,
+                            int32_t* num_prefixes);
+
+/*
+ * pcp_attn_shared_prefix — device. No counterpart on the pages: pcp_attn_varlen
+ * (flags 0) for a batch in which groups of tokens share a prefix of their keys,
+ * with each prefix's attention computed once for the whole group. A group's
+ * prefix is read once per tile of its tokens x q heads (tensor cores, the keys
+ * split over the SMs), each row's own keys from prefix_len on as usual, and the
+ * parts are merged by log-sum-exp in the call. The result is that of
+ * pcp_attn_varlen on the same rows, up to rounding.
+ * prefixes[num_prefixes], device: token ranges disjoint and ascending,
+ * prefix_len in [1, max_blocks_per_req * block_size]. A row's tokens lie inside
+ * one group or outside all of them, and a row of a group begins at or past its
+ * prefix (kv_end - q_len >= prefix_len). A group that breaks a rule is skipped
+ * with its rows, as is such a row, with *status = PCP_ERR_RANGE. num_prefixes
+ * in [0, 1024] (else PCP_ERR_ARG); with 0, prefixes may be NULL.
+ * A row of one token takes the decode path whatever its is_decode.
+ * With num_prefixes == 0 a call with num_rows >= total_q takes one-token rows
+ * only (see pcp_attn_window). FP8 cache: the descales of a prefix are those of its req.
+ * Every other argument, limit, check and error is that of pcp_attn_varlen; there
+ * are no flags. workspace: at least pcp_attn_shared_prefix_workspace_size(
+ * num_rows, num_prefixes, total_q, Hq, Hkv, D, max_blocks_per_req * block_size) bytes.
+ */
+size_t pcp_attn_shared_prefix_workspace_size(int32_t num_rows, int32_t num_prefixes, int32_t total_q,
+                                             int32_t num_q_heads, int32_t num_kv_heads,
+                                             int32_t head_dim, int32_t max_kv_len);
+int pcp_attn_shared_prefix(const void* q, const void* key_cache, const void* value_cache,
+                           const int32_t* block_table, int32_t num_reqs, int32_t max_blocks_per_req,
+                           int64_t num_blocks, int32_t block_size, const pcp_row_t* rows,
+                           int32_t num_rows, const pcp_prefix_t* prefixes, int32_t num_prefixes,
+                           int32_t total_q, int32_t num_q_heads, int32_t num_kv_heads,
+                           int32_t head_dim, float scale, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, int32_t* status, pcp_stream_t stream);
+int pcp_attn_shared_prefix_fp8kv(const void* q, const void* key_cache, const void* value_cache,
+                                 const float* k_descale, const float* v_descale,
+                                 const int32_t* block_table, int32_t num_reqs,
+                                 int32_t max_blocks_per_req, int64_t num_blocks, int32_t block_size,
+                                 const pcp_row_t* rows, int32_t num_rows, const pcp_prefix_t* prefixes,
+                                 int32_t num_prefixes, int32_t total_q, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, float scale, void* out,
+                                 float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                                 pcp_stream_t stream);
+
+/*
+ * pcp_kv_fork, pcp_kv_release, pcp_kv_compact — device. No counterpart on the
+ * pages: the bookkeeping of a paged cache whose pages are shared between
+ * requests (beam search, several samples of one prompt: the batches that
+ * pcp_attn_shared_prefix attends) or given back behind a window
+ * (pcp_attn_window). ref_count[num_blocks] counts the block-table entries that
+ * name a page; a page with a count of 0 (or less) is free. slot_bytes = Hkv * D
+ * * element size, a multiple of 16 (PCP_ERR_UNSUPPORTED otherwise); any
+ * block_size. Results do not depend on the order in which blocks run.
+ * Outputs overlap neither each other nor an input (PCP_ERR_ARG), except where
+ * said. workspace: pcp_kv_pages_workspace_size(num_blocks) bytes, 256-byte
+ * aligned, its contents on entry do not matter.
+ *
+ * pcp_kv_fork: child i continues request parent[i] of kv_len[parent[i]] tokens
+ * (parent[i] < 0: an empty child; several children of one parent are fine). Row
+ * i of block_table_out [num_children][max_blocks_per_req] names the parent's
+ * full pages, whose counts rise by one, then, where the last page is partly
+ * filled, a new page with a copy of its used slots (K and V); the other entries
+ * are -1. New pages are the lowest free ids of ref_count, in the order of the
+ * children. ref_count_out: the counts after the fork. The parents keep their
+ * pages (pcp_kv_release gives them back). *status: PCP_ERR_PAGES when no
+ * free page is left for a child (its entry is -1); PCP_ERR_RANGE for a parent
+ * >= num_reqs or of a length outside [0, max_blocks_per_req * block_size] (an
+ * empty child) and for a table entry that names no live page (-1 in the child).
+ *
+ * pcp_kv_release: entries [first_page[r], last_page[r]) of row r give one
+ * reference back each and become -1; entries that are -1 already are passed
+ * over, the others are copied. block_table_out may be block_table, and
+ * ref_count_out may be ref_count (in place). *status = PCP_ERR_RANGE for a range
+ * outside [0, max_blocks_per_req] (its row is left as it is), an id outside the
+ * pool, or a page without a reference to give back (its count stays; the entry
+ * becomes -1).
+ *
+ * pcp_kv_compact: with n live pages, the i-th live page at or above id n moves to
+ * the i-th free id below n (both ascending): K, V, count, and every entry of
+ * block_table that names it; afterwards the live pages are [0, n). Entries that
+ * name no live page become -1 (*status = PCP_ERR_RANGE for an id outside the pool
+ * that is not -1). num_live (may be NULL): n. The tables of all
+ * requests that hold pages belong in one call. Slots of pages at or above n keep
+ * their old contents.
+ * Errors of all three: PCP_ERR_ARG, PCP_ERR_ALIGN, PCP_ERR_UNSUPPORTED,
+ * PCP_ERR_WORKSPACE (nothing launched); PCP_ERR_CUDA for a failed launch.
+ */
+size_t pcp_kv_pages_workspace_size(int64_t num_blocks);
+int pcp_kv_fork(void* key_cache, void* value_cache, int64_t num_blocks, int32_t block_size,
+                int32_t slot_bytes, const int32_t* block_table, int32_t num_reqs,
+                int32_t max_blocks_per_req, const int32_t* kv_len, const int32_t* parent,
+                int32_t num_children, const int32_t* ref_count, int32_t* block_table_out,
+                int32_t* ref_count_out, void* workspace, size_t workspace_bytes, int32_t* status,
+                pcp_stream_t stream);
+int pcp_kv_release(const int32_t* block_table, int32_t num_reqs, int32_t max_blocks_per_req,
+                   const int32_t* first_page, const int32_t* last_page, const int32_t* ref_count,
+                   int64_t num_blocks, int32_t* block_table_out, int32_t* ref_count_out, int32_t* status,
+                   pcp_stream_t stream);
+int pcp_kv_compact(void* key_cache, void* value_cache, int64_t num_blocks, int32_t block_size,
+                   int32_t slot_bytes, const int32_t* block_table, int32_t num_reqs,
+                   int32_t max_blocks_per_req, const int32_t* ref_count, int32_t* block_table_out,
+                   int32_t* ref_count_out, int32_t* num_live, void* workspace, size_t workspace_bytes,
+                   int32_t* status, pcp_stream_t stream);
 
 /*
  * pcp_lse_merge — device. Merge two partial results of the same queries by
