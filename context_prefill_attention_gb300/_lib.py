@@ -3,7 +3,6 @@ step of the path runs in the library. The binding refuses to work without the
 compiled library; there is no fallback of any kind."""
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -157,13 +156,6 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _on(device: torch.device):
-    """The device of a call's tensors as the current one, where it is another."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
 def _check(rc: int, what: str):
     if rc != PCP_OK:
         raise PcpError(rc, what)
@@ -176,6 +168,7 @@ I64 = (torch.int64,)
 # an FP8 cache holds one e4m3 code per byte: raw bytes or PyTorch's e4m3 "fn" type
 FP8_CACHE = (torch.uint8,) + ((torch.float8_e4m3fn,) if hasattr(torch, "float8_e4m3fn") else ())
 
+PAGE_CACHE = BF16 + FP8_CACHE
 
 def _is_device_tensor(t: torch.Tensor) -> bool:
     return t.device.type == "cuda"
@@ -416,17 +409,6 @@ def pcp_attn_shared_prefix_workspace_size(num_rows: int, num_prefixes: int, tota
                                                             num_kv_heads, head_dim, max_kv_len))
 
 
-def _attn_buffers(q, out, lse, workspace, need: int):
-    T, hq, _ = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((hq, T), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    return out, lse, workspace
-
-
 def _i32_arg(x, name: str) -> int:
     v = int(x)
     if not -2 ** 31 <= v < 2 ** 31:
@@ -434,24 +416,83 @@ def _i32_arg(x, name: str) -> int:
     return v
 
 
+def _ready(device: int, *pairs) -> bool:
+    """Whether every ``(tensor, dtype)`` is a contiguous CUDA tensor of that type on
+    that device (the quick form of :func:`_dev`, which says what is wrong)."""
+    for t, dtype in pairs:
+        if type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+            return False
+    return True
+
+
+def _launch(f, device: int, stream, *args) -> int:
+    """``f(*args, stream)`` with the tensors' device current; without a stream, on that
+    device's current one."""
+    if device < 0:  # not a CUDA device: the library is a stand-in
+        return f(*args, _stream(stream))
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch._C._cuda_getDevice() == device:
+        return f(*args, s)
+    with torch.cuda.device(device):
+        return f(*args, s)
+
+
+def _range_args(q, key_cache, value_cache, descales, block_table, rows, out, lse, workspace, status, cache_dtypes):
+    """The checks of :func:`_check_attn` and the descales', quick where every buffer is
+    passed. Returns (T, hq, d, nb, bs, hkv, R, mb, n_rows, device index)."""
+    dev = q.get_device() if isinstance(q, torch.Tensor) else -1
+    if dev >= 0 and out is not None and lse is not None and workspace is not None:
+        cache = key_cache.dtype if isinstance(key_cache, torch.Tensor) else None
+        pairs = ((q, torch.bfloat16), (key_cache, cache), (value_cache, cache), (block_table, torch.int32),
+                 (rows, torch.int32), (out, torch.bfloat16), (lse, torch.float32), (workspace, torch.uint8))
+        if cache in cache_dtypes and _ready(dev, *pairs) and (status is None or _ready(dev, (status, torch.int32))) \
+                and (not descales or _ready(dev, (descales[0], torch.float32), (descales[1], torch.float32))):
+            qs, ks, bts, rs = q.shape, key_cache.shape, block_table.shape, rows.shape
+            if len(qs) == 3 and len(ks) == 4 and len(bts) == 2 and len(rs) == 2 and rs[1] == len(ROW_FIELDS):
+                T, hq, d = qs
+                nb, bs, hkv, kd = ks
+                R, mb = bts
+                if kd == d and value_cache.shape == ks and out.shape == qs and lse.shape == (hq, T) \
+                        and (status is None or status.numel() > 0) \
+                        and (not descales or descales[0].shape == descales[1].shape == (R, hkv)):
+                    return T, hq, d, nb, bs, hkv, R, mb, rs[0], dev
+    T, hq, d, nb, bs, hkv = _check_attn(q, key_cache, value_cache, block_table, rows, out, lse, workspace, status,
+                                        cache_dtypes)
+    R, mb = (int(x) for x in block_table.shape)
+    for t, name in zip(descales, ("k_descale", "v_descale")):
+        _dev(t, name, F32, shape=(R, hkv), device=q.device)
+    return T, hq, d, nb, bs, hkv, R, mb, int(rows.shape[0]), dev
+
+
+def _range_buffers(q, hq: int, T: int, out, lse, workspace, need):
+    """out, lse and workspace as given, or new ones (``need()``: workspace bytes)."""
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((hq, T), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(need(), 256), dtype=torch.uint8, device=q.device)
+    return out, lse, workspace
+
+
 def _attn_window(what, q, key_cache, value_cache, descales, block_table, rows, scale, window, num_sinks, out, lse,
                  workspace, status, stream, cache_dtypes):
     lib = load()
-    T, hq, d, nb, bs, hkv = _check_attn(q, key_cache, value_cache, block_table, rows, out, lse, workspace, status,
-                                        cache_dtypes)
-    R, mb, n_rows = int(block_table.shape[0]), int(block_table.shape[1]), int(rows.shape[0])
-    for t, name in zip(descales, ("k_descale", "v_descale")):
-        _dev(t, name, F32, shape=(R, hkv), device=q.device)
+    T, hq, d, nb, bs, hkv, R, mb, n_rows, dev = _range_args(q, key_cache, value_cache, descales, block_table, rows,
+                                                            out, lse, workspace, status, cache_dtypes)
     window, num_sinks = _i32_arg(window, "window"), _i32_arg(num_sinks, "num_sinks")
-    need = 0 if workspace is not None else pcp_attn_window_workspace_size(n_rows, T, hq, hkv, d, mb * bs, bs, window,
-                                                                          num_sinks)
-    out, lse, workspace = _attn_buffers(q, out, lse, workspace, need)
-    with _on(q.device):
-        rc = getattr(lib, what)(_t_ptr(q), _t_ptr(key_cache), _t_ptr(value_cache), *map(_t_ptr, descales),
-                                _t_ptr(block_table), R, mb, nb, bs, _t_ptr(rows), n_rows, T, hq, hkv, d, float(scale),
-                                window, num_sinks, _t_ptr(out), _t_ptr(lse), _t_ptr(workspace),
-                                int(workspace.numel() * workspace.element_size()), _t_ptr(status), _stream(stream))
-    _check(rc, what)
+    out, lse, workspace = _range_buffers(
+        q, hq, T, out, lse, workspace,
+        lambda: pcp_attn_window_workspace_size(n_rows, T, hq, hkv, d, mb * bs, bs, window, num_sinks))
+    rc = _launch(getattr(lib, what), dev, stream, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                 *[x.data_ptr() for x in descales], block_table.data_ptr(), R, mb, nb, bs, rows.data_ptr(), n_rows, T,
+                 hq, hkv, d, scale, window, num_sinks, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), None if status is None else status.data_ptr())
+    if rc:
+        raise PcpError(rc, what)
     return out, lse
 
 
@@ -501,20 +542,19 @@ def pcp_build_prefix_groups(rows: np.ndarray, block_table, block_size: int, min_
 def _attn_shared(what, q, key_cache, value_cache, descales, block_table, rows, prefixes, scale, out, lse, workspace,
                  status, stream, cache_dtypes):
     lib = load()
-    T, hq, d, nb, bs, hkv = _check_attn(q, key_cache, value_cache, block_table, rows, out, lse, workspace, status,
-                                        cache_dtypes)
+    T, hq, d, nb, bs, hkv, R, mb, n_rows, dev = _range_args(q, key_cache, value_cache, descales, block_table, rows,
+                                                            out, lse, workspace, status, cache_dtypes)
     _dev(prefixes, "prefixes", I32, shape=(-1, len(PREFIX_FIELDS)), device=q.device)
-    R, mb, n_rows, ng = int(block_table.shape[0]), int(block_table.shape[1]), int(rows.shape[0]), int(prefixes.shape[0])
-    for t, name in zip(descales, ("k_descale", "v_descale")):
-        _dev(t, name, F32, shape=(R, hkv), device=q.device)
-    need = 0 if workspace is not None else pcp_attn_shared_prefix_workspace_size(n_rows, ng, T, hq, hkv, d, mb * bs)
-    out, lse, workspace = _attn_buffers(q, out, lse, workspace, need)
-    with _on(q.device):
-        rc = getattr(lib, what)(_t_ptr(q), _t_ptr(key_cache), _t_ptr(value_cache), *map(_t_ptr, descales),
-                                _t_ptr(block_table), R, mb, nb, bs, _t_ptr(rows), n_rows, _t_ptr(prefixes), ng, T, hq,
-                                hkv, d, float(scale), _t_ptr(out), _t_ptr(lse), _t_ptr(workspace),
-                                int(workspace.numel() * workspace.element_size()), _t_ptr(status), _stream(stream))
-    _check(rc, what)
+    ng = prefixes.shape[0]
+    out, lse, workspace = _range_buffers(
+        q, hq, T, out, lse, workspace,
+        lambda: pcp_attn_shared_prefix_workspace_size(n_rows, ng, T, hq, hkv, d, mb * bs))
+    rc = _launch(getattr(lib, what), dev, stream, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                 *[x.data_ptr() for x in descales], block_table.data_ptr(), R, mb, nb, bs, rows.data_ptr(), n_rows,
+                 prefixes.data_ptr(), ng, T, hq, hkv, d, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), None if status is None else status.data_ptr())
+    if rc:
+        raise PcpError(rc, what)
     return out, lse
 
 
@@ -547,19 +587,37 @@ def pcp_kv_pages_workspace_size(num_blocks: int) -> int:
 
 
 def _check_pages(key_cache, value_cache, block_table, ref_count, status):
-    _dev(key_cache, "key_cache", BF16 + FP8_CACHE, shape=(-1, -1, -1, -1))
-    dev = key_cache.device
-    _dev(value_cache, "value_cache", (key_cache.dtype,), shape=tuple(key_cache.shape), device=dev)
-    nb, bs, hkv, d = (int(x) for x in key_cache.shape)
-    _dev(block_table, "block_table", I32, shape=(-1, -1), device=dev)
-    _dev(ref_count, "ref_count", I32, shape=(nb,), device=dev)
-    _status(status, dev)
+    dtype = key_cache.dtype if isinstance(key_cache, torch.Tensor) else None
+    dev = key_cache.get_device() if dtype is not None else -1
+    if dev < 0 or dtype not in PAGE_CACHE or \
+            not _ready(dev, (key_cache, dtype), (value_cache, dtype), (block_table, torch.int32),
+                       (ref_count, torch.int32)) or \
+            key_cache.dim() != 4 or value_cache.shape != key_cache.shape or block_table.dim() != 2 or \
+            ref_count.shape != key_cache.shape[:1]:
+        _dev(key_cache, "key_cache", PAGE_CACHE, shape=(-1, -1, -1, -1))
+        device = key_cache.device
+        _dev(value_cache, "value_cache", (dtype,), shape=tuple(key_cache.shape), device=device)
+        _dev(block_table, "block_table", I32, shape=(-1, -1), device=device)
+        _dev(ref_count, "ref_count", I32, shape=(int(key_cache.shape[0]),), device=device)
+    if status is not None:
+        _status(status, key_cache.device)
+    nb, bs, hkv, d = key_cache.shape
     return dev, nb, bs, hkv * d * key_cache.element_size()
 
 
-def _out_like(t, name: str, shape, device):
+def _given(t, name: str):
+    if t is None:
+        raise TypeError(f"{name}: expected a torch.Tensor, got NoneType")
+    return t
+
+
+def _i32_buffer(t, name: str, shape, device):
+    """``t`` checked as an int32 buffer of ``shape``, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=torch.int32, device=device)
+    if type(t) is torch.Tensor and t.dtype is torch.int32 and t.is_cuda and t.shape == shape and t.is_contiguous() \
+            and t.device == device:
+        return t
     return _dev(t, name, I32, shape=shape, device=device)
 
 
@@ -580,19 +638,19 @@ def pcp_kv_fork(key_cache: torch.Tensor, value_cache: torch.Tensor, block_table:
     [num_children, max_blocks], ref_count_out)``."""
     lib = load()
     dev, nb, bs, slot_bytes = _check_pages(key_cache, value_cache, block_table, ref_count, status)
-    R, mb = (int(x) for x in block_table.shape)
-    _dev(kv_len, "kv_len", I32, shape=(R,), device=dev)
-    _dev(parent, "parent", I32, shape=(-1,), device=dev)
-    N = int(parent.shape[0])
-    block_table_out = _out_like(block_table_out, "block_table_out", (N, mb), dev)
-    ref_count_out = _out_like(ref_count_out, "ref_count_out", (nb,), dev)
-    workspace = _pages_workspace(workspace, nb, dev)
-    with _on(dev):
-        rc = lib.pcp_kv_fork(_t_ptr(key_cache), _t_ptr(value_cache), nb, bs, slot_bytes, _t_ptr(block_table), R, mb,
-                             _t_ptr(kv_len), _t_ptr(parent), N, _t_ptr(ref_count), _t_ptr(block_table_out),
-                             _t_ptr(ref_count_out), _t_ptr(workspace),
-                             int(workspace.numel() * workspace.element_size()), _t_ptr(status), _stream(stream))
-    _check(rc, "pcp_kv_fork")
+    device = key_cache.device
+    R, mb = block_table.shape
+    _i32_buffer(_given(kv_len, "kv_len"), "kv_len", (R,), device)
+    N = _dev(parent, "parent", I32, shape=(-1,), device=device).shape[0]
+    block_table_out = _i32_buffer(block_table_out, "block_table_out", (N, mb), device)
+    ref_count_out = _i32_buffer(ref_count_out, "ref_count_out", (nb,), device)
+    workspace = _pages_workspace(workspace, nb, device)
+    rc = _launch(lib.pcp_kv_fork, dev, stream, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, slot_bytes,
+                 block_table.data_ptr(), R, mb, kv_len.data_ptr(), parent.data_ptr(), N, ref_count.data_ptr(),
+                 block_table_out.data_ptr(), ref_count_out.data_ptr(), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), None if status is None else status.data_ptr())
+    if rc:
+        raise PcpError(rc, "pcp_kv_fork")
     return block_table_out, ref_count_out
 
 
@@ -605,19 +663,20 @@ def pcp_kv_release(block_table: torch.Tensor, first_page: torch.Tensor, last_pag
     work in place."""
     lib = load()
     _dev(block_table, "block_table", I32, shape=(-1, -1))
-    dev = block_table.device
-    R, mb = (int(x) for x in block_table.shape)
-    _dev(first_page, "first_page", I32, shape=(R,), device=dev)
-    _dev(last_page, "last_page", I32, shape=(R,), device=dev)
-    _dev(ref_count, "ref_count", I32, shape=(-1,), device=dev)
-    _status(status, dev)
-    nb = int(ref_count.shape[0])
-    block_table_out = _out_like(block_table_out, "block_table_out", (R, mb), dev)
-    ref_count_out = _out_like(ref_count_out, "ref_count_out", (nb,), dev)
-    with _on(dev):
-        rc = lib.pcp_kv_release(_t_ptr(block_table), R, mb, _t_ptr(first_page), _t_ptr(last_page), _t_ptr(ref_count),
-                                nb, _t_ptr(block_table_out), _t_ptr(ref_count_out), _t_ptr(status), _stream(stream))
-    _check(rc, "pcp_kv_release")
+    device = block_table.device
+    R, mb = block_table.shape
+    _i32_buffer(_given(first_page, "first_page"), "first_page", (R,), device)
+    _i32_buffer(_given(last_page, "last_page"), "last_page", (R,), device)
+    nb = _dev(ref_count, "ref_count", I32, shape=(-1,), device=device).shape[0]
+    if status is not None:
+        _status(status, device)
+    block_table_out = _i32_buffer(block_table_out, "block_table_out", (R, mb), device)
+    ref_count_out = _i32_buffer(ref_count_out, "ref_count_out", (nb,), device)
+    rc = _launch(lib.pcp_kv_release, block_table.get_device(), stream, block_table.data_ptr(), R, mb,
+                 first_page.data_ptr(), last_page.data_ptr(), ref_count.data_ptr(), nb, block_table_out.data_ptr(),
+                 ref_count_out.data_ptr(), None if status is None else status.data_ptr())
+    if rc:
+        raise PcpError(rc, "pcp_kv_release")
     return block_table_out, ref_count_out
 
 
@@ -630,17 +689,18 @@ def pcp_kv_compact(key_cache: torch.Tensor, value_cache: torch.Tensor, block_tab
     int32 ``[1]`` on the device."""
     lib = load()
     dev, nb, bs, slot_bytes = _check_pages(key_cache, value_cache, block_table, ref_count, status)
-    R, mb = (int(x) for x in block_table.shape)
-    block_table_out = _out_like(block_table_out, "block_table_out", (R, mb), dev)
-    ref_count_out = _out_like(ref_count_out, "ref_count_out", (nb,), dev)
-    num_live = _out_like(num_live, "num_live", (1,), dev)
-    workspace = _pages_workspace(workspace, nb, dev)
-    with _on(dev):
-        rc = lib.pcp_kv_compact(_t_ptr(key_cache), _t_ptr(value_cache), nb, bs, slot_bytes, _t_ptr(block_table), R,
-                                mb, _t_ptr(ref_count), _t_ptr(block_table_out), _t_ptr(ref_count_out),
-                                _t_ptr(num_live), _t_ptr(workspace),
-                                int(workspace.numel() * workspace.element_size()), _t_ptr(status), _stream(stream))
-    _check(rc, "pcp_kv_compact")
+    device = key_cache.device
+    R, mb = block_table.shape
+    block_table_out = _i32_buffer(block_table_out, "block_table_out", (R, mb), device)
+    ref_count_out = _i32_buffer(ref_count_out, "ref_count_out", (nb,), device)
+    num_live = _i32_buffer(num_live, "num_live", (1,), device)
+    workspace = _pages_workspace(workspace, nb, device)
+    rc = _launch(lib.pcp_kv_compact, dev, stream, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, slot_bytes,
+                 block_table.data_ptr(), R, mb, ref_count.data_ptr(), block_table_out.data_ptr(),
+                 ref_count_out.data_ptr(), num_live.data_ptr(), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), None if status is None else status.data_ptr())
+    if rc:
+        raise PcpError(rc, "pcp_kv_compact")
     return block_table_out, ref_count_out, num_live
 
 

@@ -30,6 +30,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "pcp_device.cuh"
 #include "pcp_internal.h"
 
@@ -449,51 +451,78 @@ __global__ void __launch_bounds__(256)
 // a prefix group one for its own keys (partial nparts - 1 of part_out); the rows
 // of a group also those of the prefix's shards (partials 0 .. shards - 1). A
 // longer row outside every group was written by the packed kernel.
+//
+// One warp per (token, head): lane l holds D / 32 dims. The partials are taken in
+// batches of kMergeBatch whose loads (lse and values together) are all in flight at
+// once; a running maximum joins the batches.
+constexpr int kMergeBatch = 8;
 template <int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(256)
     range_merge_kernel(PrefillArgs a, const int32_t* __restrict__ row_grp, const int32_t* __restrict__ grp_shards,
                        const float* __restrict__ dec_out, const float* __restrict__ dec_lse, int max_splits,
                        int parts_per_split) {
-    const int ri = blockIdx.x, h = blockIdx.y, d = threadIdx.x;
-    if (!a.row_ok[ri]) return;
+    constexpr int kV = D / 32;
+    using Vec = typename std::conditional<kV == 4, float4, float2>::type;
+    grid_wait();
+    const int ri = blockIdx.x, lane = threadIdx.x % 32;
+    const int h = blockIdx.y * 8 + threadIdx.x / 32;
+    if (h >= a.hq || !a.row_ok[ri]) return;
     const pcp_row_t row = a.rows[ri];
     const int32_t grp = row_grp[ri];
     if (row.q_len > 1 && grp < 0) return;
     const int shards = grp >= 0 ? grp_shards[grp] : 0;
-    int n = 0;  // partials of the row's own keys in dec_out
-    if (row.q_len == 1) n = parts_per_split * ((key_range(a, row, a.row_lo[ri]).len + a.chunk - 1) / a.chunk);
+    const bool one = row.q_len == 1;
+    // partials 0 .. n - 1 are the row's own keys', the others the prefix's shards
+    const int n = one ? parts_per_split * ((key_range(a, row, a.row_lo[ri]).len + a.chunk - 1) / a.chunk) : 1;
     const size_t base = ((size_t)ri * a.hq + h) * (2 * max_splits);
     const size_t out_stride = (size_t)a.total_q * a.hq * D, lse_stride = (size_t)a.hq * a.total_q;
     // tokens of a longer row are dealt over gridDim.z
     for (int32_t t = row.q_start + blockIdx.z; t < row.q_start + row.q_len; t += gridDim.z) {
-        const size_t li = (size_t)h * a.total_q + t, o = ((size_t)t * a.hq + h) * D + d;
-        const bool own = row.q_len > 1;  // partial nparts - 1 holds the own keys
-        float M = own ? a.part_lse[(size_t)(a.nparts - 1) * lse_stride + li] : -INFINITY;
-#pragma unroll 8
-        for (int s = 0; s < n; ++s) M = fmaxf(M, dec_lse[base + s]);
-#pragma unroll 8
-        for (int s = 0; s < shards; ++s) M = fmaxf(M, a.part_lse[(size_t)s * lse_stride + li]);
-        float W = 0.f, O = 0.f;
-        if (M != -INFINITY) {
-            if (own) {
-                W = __expf(a.part_lse[(size_t)(a.nparts - 1) * lse_stride + li] - M);
-                O = W * a.part_out[(size_t)(a.nparts - 1) * out_stride + o];
+        const size_t li = (size_t)h * a.total_q + t, o = ((size_t)t * a.hq + h) * D;
+        float M = -INFINITY, W = 0.f, O[kV] = {};
+        for (int s0 = 0; s0 < n + shards; s0 += kMergeBatch) {
+            float ls[kMergeBatch];
+            Vec x[kMergeBatch];
+#pragma unroll
+            for (int k = 0; k < kMergeBatch; ++k) {
+                const int s = s0 + k;
+                ls[k] = -INFINITY;
+                if (s >= n + shards) continue;
+                if (one && s < n) {
+                    ls[k] = __ldcg(dec_lse + base + s);
+                    x[k] = __ldcg(reinterpret_cast<const Vec*>(dec_out + (base + s) * D) + lane);
+                } else {
+                    const size_t p = s < n ? a.nparts - 1 : s - n;
+                    ls[k] = __ldcg(a.part_lse + p * lse_stride + li);
+                    x[k] = __ldcg(reinterpret_cast<const Vec*>(a.part_out + p * out_stride + o) + lane);
+                }
             }
-#pragma unroll 8
-            for (int s = 0; s < n; ++s) {
-                const float w = __expf(dec_lse[base + s] - M);
+            float m = M;
+#pragma unroll
+            for (int k = 0; k < kMergeBatch; ++k) m = fmaxf(m, ls[k]);
+            if (m == -INFINITY) continue;
+            const float f = __expf(M - m);
+            W *= f;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) O[e] *= f;
+            M = m;
+#pragma unroll
+            for (int k = 0; k < kMergeBatch; ++k) {
+                if (ls[k] == -INFINITY) continue;
+                const float w = __expf(ls[k] - M);
                 W += w;
-                O += w * dec_out[(base + s) * D + d];
-            }
-#pragma unroll 8
-            for (int s = 0; s < shards; ++s) {
-                const float w = __expf(a.part_lse[(size_t)s * lse_stride + li] - M);
-                W += w;
-                O += w * a.part_out[(size_t)s * out_stride + o];
+                const float* v = reinterpret_cast<const float*>(&x[k]);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) O[e] += w * v[e];
             }
         }
-        reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(W > 0.f ? O / W : 0.f);
-        if (d == 0) a.lse[li] = W > 0.f ? M + __logf(W) : -INFINITY;
+        const float inv = W > 0.f ? 1.f / W : 0.f;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + o) + lane * (kV / 2);
+        if constexpr (kV == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
+        else
+            *dst = pack_bf16x2(O[0] * inv, O[1] * inv);
+        if (lane == 0) a.lse[li] = W > 0.f ? M + __logf(W) : -INFINITY;
     }
 }
 
@@ -597,13 +626,13 @@ int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32
                        const float* dec_out, const float* dec_lse, int32_t max_splits, int parts,
                        cudaStream_t stream) {
     // longer rows have tokens for several blocks; where no row can be longer than
-    // one token (num_rows == total_q) one block per (row, head) does
-    const dim3 grid(a.num_rows, a.hq, a.total_q > a.num_rows && a.num_prefixes > 0 ? 16 : 1);
-    if (a.d == 64)
-        range_merge_kernel<64><<<grid, 64, 0, stream>>>(a, row_grp, grp_shards, dec_out, dec_lse, max_splits, parts);
-    else
-        range_merge_kernel<128><<<grid, 128, 0, stream>>>(a, row_grp, grp_shards, dec_out, dec_lse, max_splits, parts);
-    const cudaError_t e = cudaGetLastError();
+    // one token (num_rows == total_q) one block per row and eight heads does
+    const dim3 grid(a.num_rows, (a.hq + 7) / 8, a.total_q > a.num_rows && a.num_prefixes > 0 ? 16 : 1);
+    const cudaError_t e =
+        a.d == 64 ? launch_chained(range_merge_kernel<64>, grid, dim3(256), 0, stream, a, row_grp, grp_shards, dec_out,
+                                   dec_lse, max_splits, parts)
+                  : launch_chained(range_merge_kernel<128>, grid, dim3(256), 0, stream, a, row_grp, grp_shards, dec_out,
+                                   dec_lse, max_splits, parts);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }

@@ -361,8 +361,9 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                      float* __restrict__ dec_lse, int max_splits, int q_rows) {
     using C = TcCfg<F8, GP>;
     constexpr int kKS = C::kKS, kVS = C::kVS, kNS = C::kNS;
-    const int32_t total = a.num_units[1];
-    if ((int32_t)blockIdx.x >= total) return;
+    if constexpr (!RNG) {
+        if ((int32_t)blockIdx.x >= a.num_units[1]) return;
+    }
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -408,7 +409,6 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
     };
     const int32_t* tail_rows = a.dec_pre + a.num_rows + 1;
 
-    for (int i = threadIdx.x; i <= a.num_rows; i += tc_threads(F8, GP)) pre[i] = a.dec_pre[i];
     if (threadIdx.x == 0) {
         const uint32_t filled = F8 ? 4 : 1;  // FP8: each warp of the converter set arrives
         for (int s = 0; s < kKS; ++s) {
@@ -442,6 +442,13 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
+    // RNG: launched behind the scheduler, whose work list is read from here on
+    if constexpr (RNG) {
+        grid_wait();
+        grid_launch_dependents();
+    }
+    for (int i = threadIdx.x; i <= a.num_rows; i += tc_threads(F8, GP)) pre[i] = a.dec_pre[i];
+    const int32_t total = a.num_units[1];
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -858,9 +865,14 @@ int launch_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_
         cudaFuncSetAttribute(decode_tc_kernel<F8, GP, RNG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     const int ctas = grid > 0 && grid < num_sms() ? grid : num_sms();
-    decode_tc_kernel<F8, GP, RNG><<<ctas, tc_threads(F8, GP), smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
-                                                                              max_splits, q_rows);
-    e = cudaGetLastError();
+    if (RNG) {
+        e = launch_chained(decode_tc_kernel<F8, GP, RNG>, dim3(ctas), dim3(tc_threads(F8, GP)), smem, stream, tq, tk, tv,
+                           a, dec_out, dec_lse, max_splits, q_rows);
+    } else {
+        decode_tc_kernel<F8, GP, RNG><<<ctas, tc_threads(F8, GP), smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
+                                                                                  max_splits, q_rows);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }

@@ -180,47 +180,51 @@ __device__ __forceinline__ Item decode_item(const Unit* units, int32_t idx, int3
     return it;
 }
 
-// Item idx of a packed call (pcp_attn_window, pcp_attn_shared_prefix): a unit's
-// tokens for one kv head. A tile's 128 MMA rows are tpt = 128 / G tokens x the
-// head's G q heads (row r: token r / G, q head r % G), so a row of few tokens
-// fills its tiles, and the keys a tile needs beyond the window are those of tpt
-// tokens, not of 128; the item's head slots are slots consecutive tiles of one
-// row that share the K/V stream. row >= num_rows names prefix group
-// row - num_rows, whose tokens all see exactly the keys [k_lo, k_hi).
-// The keys are walked as whole pages back to back: those of the sinks that lie
-// before the window, then those from the window's first key k_lo on. Slot v of
-// that walk is key v below the sinks' last page end, key v + shift after it.
-// kb holds the number of sink slots, k_end the walk's length, rows_valid tokens.
-__device__ __forceinline__ Item packed_item(const PrefillArgs& a, const Unit& u, int32_t hk, int32_t G) {
-    const int32_t bs = a.block_size, span = a.slots * (kBlockM / G);
+// The packed unit of tokens [mt * span, ...) of a row (or prefix group) for the
+// keys [k_lo, k_hi) (pcp_attn_window, pcp_attn_shared_prefix); an item is a unit
+// for one kv head. A tile's 128 MMA rows are tpt = 128 / G tokens x the head's G
+// q heads (row r: token r / G, q head r % G), so a row of few tokens fills its
+// tiles, and the keys a tile needs beyond the window are those of tpt tokens,
+// not of 128; the item's head slots are a.slots consecutive tiles of the row
+// that share the K/V stream (span tokens in all). The keys are walked as whole
+// pages back to back: those of the sinks that lie before the window, then those
+// from the window's first key on. Slot v of that walk is key v below the sinks'
+// last page end, key v + shift after it.
+__device__ __forceinline__ PackedUnit packed_unit(const PrefillArgs& a, int32_t req, int32_t q_start, int32_t q_len,
+                                                  int32_t first_pos, int32_t mt, int32_t span, int32_t k_lo,
+                                                  int32_t k_hi, int32_t pass) {
+    const int32_t bs = a.block_size;
+    PackedUnit u;
+    u.req = req;
+    u.q_tok0 = q_start + mt * span;
+    const int32_t tokens = min(span, q_len - mt * span);
+    u.tokens_pass = tokens | (pass << 16);
+    u.pos0 = first_pos + mt * span;
+    u.k_lo = max(k_lo, u.pos0 - a.window + 1);
+    u.k_hi = k_hi;
+    const int32_t sink_slots = (min(a.sinks, u.k_lo) + bs - 1) / bs * bs;
+    u.shift = max(0, u.k_lo / bs * bs - sink_slots);
+    u.k_end = min(k_hi, u.pos0 + tokens) - u.shift;
+    return u;
+}
+
+__device__ __forceinline__ Item packed_item(const PrefillArgs& a, int32_t idx) {
+    const int32_t n = idx / a.hkv;
+    const int4* src = reinterpret_cast<const int4*>(a.packed + n);
+    const int4 x = __ldcg(src), y = __ldcg(src + 1);
     Item it{};
     it.nslots = a.slots;
-    it.hk = hk;
-    it.h0 = hk * G;
-    const int32_t mt = u.mt_pass & 0xFFFFFF;
-    it.pass = u.mt_pass >> 24;
-    it.k_hi = u.k_hi;
-    if (u.row >= 0 && u.row < a.num_rows) {
-        const pcp_row_t r = a.rows[u.row];
-        it.req = r.req;
-        it.q_tok0 = r.q_start + mt * span;
-        it.rows_valid = min(span, r.q_len - mt * span);
-        it.pos0 = r.kv_end - r.q_len + mt * span;
-        it.k_lo = max(u.k_lo, it.pos0 - a.window + 1);
-    } else if (u.row >= a.num_rows && u.row - a.num_rows < a.num_prefixes) {
-        const pcp_prefix_t g = a.prefixes[u.row - a.num_rows];
-        it.req = g.req;
-        it.q_tok0 = g.q_start + mt * span;
-        it.rows_valid = min(span, g.q_len - mt * span);
-        it.pos0 = u.k_hi;  // every query lies past the prefix
-        it.k_lo = u.k_lo;
-    } else {
-        return it;  // never written by the scheduler: an empty item
-    }
-    const int32_t sinks = min(a.sinks, it.k_lo);
-    it.kb = (sinks + bs - 1) / bs * bs;
-    it.shift = max(0, it.k_lo / bs * bs - it.kb);
-    it.k_end = min(u.k_hi, it.pos0 + it.rows_valid) - it.shift;
+    it.hk = idx - n * a.hkv;
+    it.h0 = it.hk * (a.hq / a.hkv);
+    it.req = x.x;
+    it.q_tok0 = x.y;
+    it.rows_valid = x.z & 0xFFFF;  // tokens
+    it.pass = x.z >> 16;
+    it.pos0 = x.w;
+    it.k_lo = y.x;
+    it.k_hi = y.y;
+    it.shift = y.z;
+    it.k_end = y.w;  // in slots
     it.n_tiles = it.k_end > 0 ? (it.k_end + kBlockN - 1) / kBlockN : 0;
     return it;
 }
@@ -479,6 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // PACK: this block may run while the decode kernel still does: nothing read or
+    // written here is that kernel's, and each of its blocks has waited for the
+    // scheduler, whose results are therefore in memory (the fence drops any older
+    // copy in this SM's L1)
+    if constexpr (PACK) {
+        __threadfence();
+        grid_launch_dependents();
+    }
     const int32_t total_items = (*a.num_units) * slots_per_unit;
     // Item of this CTA in round r: the longest-first list is dealt out in snake
     // order (forward on even rounds, backward on odd ones), which balances the
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return r * (int32_t)gridDim.x + ((r & 1) ? (int32_t)(gridDim.x - 1 - blockIdx.x) : (int32_t)blockIdx.x);
     };
     auto item_at = [&](int32_t idx) -> Item {
-        if constexpr (PACK) return packed_item(a, a.units[idx / slots_per_unit], idx % slots_per_unit, G);
+        if constexpr (PACK) return packed_item(a, idx);
         else return decode_item(a.units, idx, slots_per_unit, dual, G, a.rows, a.num_rows, bs);
     };
     // Registers: the launch gives 168 per thread (384 threads); the producer /
@@ -524,13 +536,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     qbar, h * 64, PACK ? it.h0 : it.h0 + g, PACK ? it.q_tok0 + g * tpt : it.q_tok0);
             }
             const int32_t* table = a.block_table + (size_t)it.req * a.max_blocks;
+            // PACK: slots from the sinks' last page end on are shift keys further
+            const int32_t sink_slots = PACK ? (min(a.sinks, it.k_lo) + bs - 1) / bs * bs : 0;
             for (int32_t j = 0; j < it.n_tiles && ok; ++j) {
                 // this lane's page -> first cache row of the page; pages past k_end (and
                 // bad ids) map to a row past the cache, which TMA fills with zeros
                 int32_t y = oob;
                 const int32_t k = (PACK ? 0 : it.kb) + j * kBlockN + lane * bs;
                 if (lane < pages && k < it.k_end) {
-                    const int32_t pg = (PACK && k >= it.kb ? k + it.shift : k) / bs;
+                    const int32_t pg = (PACK && k >= sink_slots ? k + it.shift : k) / bs;
                     const int32_t id = pg < a.max_blocks ? __ldg(table + pg) : -1;
                     if (id >= 0 && id < a.num_blocks) y = id * bs;
                     else report_status(a.status, PCP_ERR_RANGE);
@@ -745,6 +759,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = PACK ? r < tpt * G && tl < it.rows_valid : r < it.rows_valid;
             const int32_t pos = it.pos0 + min(PACK ? tl : r, it.rows_valid - 1);
             const int32_t tok = it.q_tok0 + (PACK ? tl : r);
+            // PACK: slots [full_lo, full_hi) are keys that every query of the item sees
+            const int32_t full_lo = PACK ? max(it.k_lo, it.pos0 + it.rows_valid - a.window) - it.shift : 0;
+            const int32_t full_hi = PACK ? min(it.k_hi, it.pos0 + 1) - it.shift : 0;
             float m = -INFINITY, l = 0.f;
             const int n = it.n_tiles;
             const uint32_t vt0 = vt_all;  // tiles before this item: V(j) is in stage (vt0 + j) % kNV
@@ -780,17 +797,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t s[128];
                 float* sf = reinterpret_cast<float*>(s);
                 const float sl2 = F8 ? a.scale * __ldg(kd_ptr) * kLog2e * qs_row : a.scale * kLog2e;
-                // PACK: key0 counts slots of the walk less the shift, so that a slot past the
-                // sinks is compared as the key it holds
-                const int32_t key0 = PACK ? j * kBlockN + it.shift : it.kb + j * kBlockN;
-                const bool full = key0 >= (PACK ? max(it.k_lo, it.pos0 + it.rows_valid - a.window) : it.k_lo) &&
-                                  key0 + kBlockN <= it.k_hi && key0 + kBlockN - 1 <= it.pos0;
-                // keys outside [k_lo, min(k_hi, pos + 1)) of the tile's columns [c0, 128) at -inf;
-                // PACK: the row's own window, and the sinks
+                const int32_t key0 = PACK ? j * kBlockN : it.kb + j * kBlockN;
+                const bool full = PACK ? key0 >= full_lo && key0 + kBlockN <= full_hi
+                                       : key0 >= it.k_lo && key0 + kBlockN <= it.k_hi && key0 + kBlockN - 1 <= it.pos0;
+                // keys outside [k_lo, min(k_hi, pos + 1)) of the tile's columns [c0, 128) at -inf.
+                // PACK: in slots, the row's own window and the sinks; its bounds are read again
+                // here, in the few tiles that need them, rather than held in registers
                 auto mask_scores = [&](float* x, auto c0) {
-                    const int32_t lo = (PACK ? max(it.k_lo, pos - a.window + 1) : it.k_lo) - key0;
-                    const int32_t hi = min(it.k_hi, pos + 1) - key0;
-                    const int32_t sk = PACK ? a.sinks - j * kBlockN : 0;
+                    int32_t lo = it.k_lo - key0, hi = min(it.k_hi, pos + 1) - key0, sk = 0;
+                    if constexpr (PACK) {
+                        const Item m_it = item_at(idx);
+                        const int32_t m_pos = m_it.pos0 + min(g * tpt + r / G, m_it.rows_valid - 1);
+                        lo = max(m_it.k_lo, m_pos - a.window + 1) - m_it.shift - key0;
+                        hi = min(m_it.k_hi, m_pos + 1) - m_it.shift - key0;
+                        sk = a.sinks - key0;
+                    }
 #pragma unroll
                     for (int c2 = decltype(c0)::value; c2 < 128; ++c2)
                         if ((c2 < lo && (!PACK || c2 >= sk)) || c2 >= hi) x[c2] = -INFINITY;
@@ -816,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (cache rows before the window, unwritten ones past the end) before its
                     // P, and with it this tile's first PV, is released; S(j) done means that
                     // V(j) has landed
-                    if (g == 0 && !full && !packed_slot_live(it, a.sinks, j * kBlockN + r)) {
+                    if (g == 0 && !full && !packed_slot_live(item_at(idx), a.sinks, key0 + r)) {
                         uint8_t* vrow = smem + C::kV + ((vt0 + j) % kNV) * C::kTileBytes + r * 128;
 #pragma unroll
                         for (int h2 = 0; h2 < C::kHalves; ++h2)
@@ -955,7 +976,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
             }
-            const size_t orow = ((size_t)tok * a.hq + h) * D;
+            // PACK: the unit's fields again, for the same reason
+            const Item e_it = PACK ? item_at(idx) : it;
+            const int32_t e_tl = PACK ? g * tpt + r / G : 0;
+            const int32_t e_tok = PACK ? e_it.q_tok0 + e_tl : tok, e_h = PACK ? e_it.h0 + r % G : h;
+            const bool e_valid = PACK ? r < tpt * G && e_tl < e_it.rows_valid : valid;
+            const size_t orow = ((size_t)e_tok * a.hq + e_h) * D;
             // the whole O row into registers first, so the accumulator can be handed
             // back to the MMA warp (next item) before the global stores
             uint32_t orow_regs[D];
@@ -973,8 +999,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c2 = 0; c2 < D / 32; ++c2) {
                 const uint32_t* o = &orow_regs[32 * c2];
-                if (valid) {
-                    if (it.pass == 0) {
+                if (e_valid) {
+                    if (e_it.pass == 0) {
                         uint4* dst = reinterpret_cast<uint4*>(
                             reinterpret_cast<__nv_bfloat16*>(a.out) + orow + 32 * c2);
 #pragma unroll
@@ -988,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
                         float4* dst = reinterpret_cast<float4*>(
-                            a.part_out + (size_t)(it.pass - 1) * a.total_q * a.hq * D + orow + 32 * c2);
+                            a.part_out + (size_t)(e_it.pass - 1) * a.total_q * a.hq * D + orow + 32 * c2);
 #pragma unroll
                         for (int v4 = 0; v4 < 8; ++v4)
                             dst[v4] = make_float4(__uint_as_float(o[4 * v4 + 0]) * inv, __uint_as_float(o[4 * v4 + 1]) * inv,
@@ -996,15 +1022,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (valid) {
-                float* lse_dst = it.pass == 0 ? a.lse : a.part_lse + (size_t)(it.pass - 1) * a.hq * a.total_q;
-                lse_dst[(size_t)h * a.total_q + tok] = lse_v;
+            if (e_valid) {
+                float* lse_dst = e_it.pass == 0 ? a.lse : a.part_lse + (size_t)(e_it.pass - 1) * a.hq * a.total_q;
+                lse_dst[(size_t)e_h * a.total_q + e_tok] = lse_v;
             }
         }
         if (!ok) report_status(a.status, PCP_ERR_TIMEOUT);
     }
 
     __syncwarp();  // lane 0 of the producer and of the MMA warp worked alone: reconverge first
+    // PACK: this kernel ends after the decode kernel, so that what follows it may
+    // read both their results
+    if constexpr (PACK) grid_wait();
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -1070,8 +1099,8 @@ constexpr int kTailBuckets = kDecodeChunk / kBlockN;
 
 // units[0, n) into sorted by descending cost (key tiles), by the whole block;
 // keys: kSortCap entries of shared memory.
-template <typename Cost>
-__device__ __forceinline__ void sort_units(const Unit* units, Unit* sorted, int32_t n, unsigned long long* keys,
+template <typename U, typename Cost>
+__device__ __forceinline__ void sort_units(const U* units, U* sorted, int32_t n, unsigned long long* keys,
                                            int32_t* warp_sums, Cost cost_of) {
     if (n > kSortCap) {
         // Counting sort, longest first: class c = kCostBuckets - 1 - min(cost,
@@ -1102,7 +1131,7 @@ __device__ __forceinline__ void sort_units(const Unit* units, Unit* sorted, int3
         }
         __syncthreads();
         for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
-            const Unit u = units[i];
+            const U u = units[i];
             const int32_t c = kCostBuckets - 1 - min(cost_of(u), kCostBuckets - 1);
             sorted[atomicAdd(&cnt[c], 1)] = u;
         }
@@ -1135,6 +1164,35 @@ __device__ __forceinline__ void sort_units(const Unit* units, Unit* sorted, int3
     for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) sorted[i] = units[(int32_t)(keys[i] & 0xFFFFFFFFu)];
 }
 
+// Place of this thread's row among the rows with a partial last split: after every
+// row of a longer bucket, and in row order within its bucket b (0: no such row),
+// so that the list, and with it every sum's order, is the same in every run.
+// Called by the whole block, once per kSchedThreads rows in row order; fill[]
+// (shared, zeroed) counts the rows placed so far, warp_cnt is scratch.
+__device__ __forceinline__ int32_t tail_place(int32_t b, const int32_t* off, int32_t* fill,
+                                              int32_t (*warp_cnt)[kTailBuckets + 1]) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    for (int i = threadIdx.x; i < (kSchedThreads / 32) * (kTailBuckets + 1); i += kSchedThreads)
+        (&warp_cnt[0][0])[i] = 0;
+    __syncthreads();
+    const uint32_t same = __match_any_sync(0xffffffffu, b);
+    if (lane == __ffs(same) - 1) warp_cnt[warp][b] = __popc(same);
+    __syncthreads();
+    if (threadIdx.x <= kTailBuckets) {  // running counts over the warps
+        int32_t n = fill[threadIdx.x];
+        for (int w = 0; w < kSchedThreads / 32; ++w) {
+            const int32_t c = warp_cnt[w][threadIdx.x];
+            warp_cnt[w][threadIdx.x] = n;
+            n += c;
+        }
+        fill[threadIdx.x] = n;
+    }
+    __syncthreads();
+    const int32_t at = off[b] + warp_cnt[warp][b] + __popc(same & ((1u << lane) - 1));
+    __syncthreads();
+    return at;
+}
+
 // Check every row, then build the prefill work list: one unit per (valid
 // non-decode row, 128-token tile, pass), ordered by the number of key tiles,
 // longest first. Also lays out the decode work items (kv head x kDecodeChunk-key
@@ -1149,6 +1207,7 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
     // decode rows with a partial last split per bucket, their first list
     // position, and the positions taken so far
     __shared__ int32_t tail_cnt[kTailBuckets + 1], tail_off[kTailBuckets + 1], tail_fill[kTailBuckets + 1];
+    __shared__ int32_t tail_warp[kSchedThreads / 32][kTailBuckets + 1];
     if (threadIdx.x <= kTailBuckets) {
         tail_cnt[threadIdx.x] = 0;
         tail_fill[threadIdx.x] = 0;
@@ -1215,20 +1274,22 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
             tail_off[b] = t;
             t += tail_cnt[b];
         }
+        tail_off[0] = 0;
         header[0] = n;
         header[1] = dbase + t * a.hkv;
         dec_pre[num_rows] = dbase;
     }
     __syncthreads();
-    // the rows with a partial last split, longest first (any order within a
-    // bucket: every item writes only its own partial, so the order changes no result)
-    for (int32_t ri = threadIdx.x; ri < num_rows; ri += kSchedThreads) {
-        if (!row_ok[ri]) continue;
-        const pcp_row_t row = rows[ri];
-        const int32_t part = row.kv_end % kDecodeChunk;
-        if (!row.is_decode || !part) continue;
-        const int b = (part + kBlockN - 1) / kBlockN;
-        dec_pre[num_rows + 1 + tail_off[b] + atomicAdd(&tail_fill[b], 1)] = ri;
+    // the rows with a partial last split, longest first
+    for (int32_t r0 = 0; r0 < num_rows; r0 += kSchedThreads) {
+        const int32_t ri = r0 + threadIdx.x;
+        int32_t b = 0;
+        if (ri < num_rows && row_ok[ri]) {
+            const pcp_row_t row = rows[ri];
+            if (row.is_decode) b = (row.kv_end % kDecodeChunk + kBlockN - 1) / kBlockN;
+        }
+        const int32_t at = tail_place(b, tail_off, tail_fill, tail_warp);
+        if (b) dec_pre[num_rows + 1 + at] = ri;
     }
     // every thread's units[] writes must be visible before any thread reads them
     __syncthreads();
@@ -1246,12 +1307,14 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
 // group attends all its keys into the result at once. row_lo: each row's first
 // own key; row_grp: its group or -1; grp_shards: each group's shards (0: bad).
 __global__ void __launch_bounds__(kSchedThreads, 1)
-    range_schedule_kernel(PrefillArgs a, Unit* units, Unit* sorted, int32_t* header, int32_t* row_ok,
+    range_schedule_kernel(PrefillArgs a, PackedUnit* units, PackedUnit* sorted, int32_t* header, int32_t* row_ok,
                           int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
                           int64_t max_units) {
     __shared__ int32_t warp_sums[32];
     __shared__ int32_t tail_cnt[kTailBuckets + 1], tail_off[kTailBuckets + 1], tail_fill[kTailBuckets + 1];
+    __shared__ int32_t tail_warp[kSchedThreads / 32][kTailBuckets + 1];
     __shared__ __align__(16) unsigned long long keys[kSortCap];
+    grid_launch_dependents();  // the decode kernel sets itself up meanwhile
     if (threadIdx.x <= kTailBuckets) {
         tail_cnt[threadIdx.x] = 0;
         tail_fill[threadIdx.x] = 0;
@@ -1316,12 +1379,8 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         const int32_t off = base + block_exclusive_scan(cnt, warp_sums, &tot);
         for (int32_t u = 0; u < cnt; ++u) {
             if (off + u >= max_units) break;
-            Unit x;
-            x.row = ri;
-            x.mt_pass = u | ((grp >= 0 ? a.nparts : 0) << 24);
-            x.k_lo = lo;
-            x.k_hi = row.kv_end;
-            units[off + u] = x;
+            units[off + u] = packed_unit(a, row.req, row.q_start, row.q_len, row.kv_end - row.q_len, u, span, lo,
+                                         row.kv_end, grp >= 0 ? a.nparts : 0);
         }
         base += tot;
     }
@@ -1340,11 +1399,13 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         for (int32_t u = 0; u < cnt; ++u) {
             if (off + u >= max_units) break;
             const int32_t sh = u % shards;
-            Unit x;
-            x.row = num_rows + g;
-            x.mt_pass = (u / shards) | ((1 + sh) << 24);
-            x.k_lo = (int32_t)((int64_t)pages * sh / shards) * bs;
-            x.k_hi = min(p.prefix_len, (int32_t)((int64_t)pages * (sh + 1) / shards) * bs);
+            const int32_t k_lo = (int32_t)((int64_t)pages * sh / shards) * bs;
+            const int32_t k_hi = (int32_t)min((int64_t)p.prefix_len, (int64_t)pages * (sh + 1) / shards * bs);
+            PackedUnit x = packed_unit(a, p.req, p.q_start, p.q_len, 0, u / shards, span, k_lo, k_hi, 1 + sh);
+            x.pos0 = k_hi;  // every query lies past the prefix
+            x.k_lo = k_lo;
+            x.shift = k_lo;
+            x.k_end = k_hi - k_lo;
             units[off + u] = x;
         }
         base += tot;
@@ -1357,23 +1418,25 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
             tail_off[b] = t;
             t += tail_cnt[b];
         }
+        tail_off[0] = 0;
         header[0] = n;
         header[1] = dbase + t * a.hkv;
         dec_pre[num_rows] = dbase;
     }
     __syncthreads();
-    for (int32_t ri = threadIdx.x; ri < num_rows; ri += kSchedThreads) {
-        if (!row_ok[ri]) continue;
-        const pcp_row_t row = a.rows[ri];
-        if (row.q_len != 1) continue;
-        const int32_t part = key_range(a, row, row_lo[ri]).len % a.chunk;
-        if (!part) continue;
-        const int b = (part + kBlockN - 1) / kBlockN;
-        dec_pre[num_rows + 1 + tail_off[b] + atomicAdd(&tail_fill[b], 1)] = ri;
+    for (int32_t r0 = 0; r0 < num_rows; r0 += kSchedThreads) {
+        const int32_t ri = r0 + threadIdx.x;
+        int32_t b = 0;
+        if (ri < num_rows && row_ok[ri]) {
+            const pcp_row_t row = a.rows[ri];
+            if (row.q_len == 1) b = (key_range(a, row, row_lo[ri]).len % a.chunk + kBlockN - 1) / kBlockN;
+        }
+        const int32_t at = tail_place(b, tail_off, tail_fill, tail_warp);
+        if (b) dec_pre[num_rows + 1 + at] = ri;
     }
-    __syncthreads();
-    const int32_t G = a.hq / a.hkv;
-    sort_units(units, sorted, n, keys, warp_sums, [&](const Unit& u) { return packed_item(a, u, 0, G).n_tiles; });
+    if (n > 0)
+        sort_units(units, sorted, n, keys, warp_sums,
+                   [&](const PackedUnit& u) { return (u.k_end + kBlockN - 1) / kBlockN; });
 }
 
 // ---------------------------------------------------------------- tensor maps
@@ -1442,8 +1505,12 @@ int launch_prefill_d(const PrefillArgs& a, cudaStream_t stream, int grid) {
     // persistent: the work list is dealt over however many CTAs run (fewer when
     // the decode rows take some SMs beside it)
     const int ctas = grid > 0 && grid < num_sms() ? grid : num_sms();
-    prefill_kernel<D, F8, PACK><<<ctas, kThreads, smem, stream>>>(tq, tk, tv, a);
-    e = cudaGetLastError();
+    if (PACK) {
+        e = launch_chained(prefill_kernel<D, F8, PACK>, dim3(ctas), dim3(kThreads), smem, stream, tq, tk, tv, a);
+    } else {
+        prefill_kernel<D, F8, PACK><<<ctas, kThreads, smem, stream>>>(tq, tk, tv, a);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }
@@ -1471,7 +1538,7 @@ int launch_schedule(const PrefillArgs& a, int32_t flags, Unit* units, Unit* unit
     return PCP_OK;
 }
 
-int launch_range_schedule(const PrefillArgs& a, Unit* units, Unit* units_sorted, int32_t* header, int32_t* row_ok,
+int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header, int32_t* row_ok,
                           int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
                           int64_t max_units, cudaStream_t stream) {
     range_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(a, units, units_sorted, header, row_ok, row_lo, row_grp,

@@ -29,6 +29,16 @@ struct Unit {
     int32_t k_hi;
 };
 
+// A unit of the window and shared-prefix calls' packed work list (packed_unit in
+// attn_prefill.cu), with everything its items need; items are units x kv heads.
+struct alignas(16) PackedUnit {
+    int32_t req, q_tok0;
+    int32_t tokens_pass;  // tokens | pass << 16
+    int32_t pos0;         // position of the first token
+    int32_t k_lo, k_hi;   // keys
+    int32_t shift, k_end;  // slots of the walk: key = slot + shift past the sinks; its length
+};
+
 // Workspace layout of pcp_attn_varlen (all offsets 256-byte aligned).
 struct WorkspaceLayout {
     size_t header;        // int32[64]: [0] = number of units
@@ -105,12 +115,32 @@ struct PrefillArgs {
     int32_t chunk;              // keys per decode split, a multiple of 128, at most kDecodeChunk
     int32_t window, sinks;      // keys a query sees: the last `window` ones and the first `sinks`
     int32_t slots;              // token tiles per packed item: 1 or 2
+    const PackedUnit* packed;   // the packed work list, longest first
     const int32_t* row_lo;      // first own key of each row (0, or its group's prefix length)
     const pcp_prefix_t* prefixes;
     int32_t num_prefixes;
 };
 
 #ifdef __CUDACC__
+// Launch a kernel that may start while the one before it on the stream still
+// runs (it calls grid_wait before it touches that one's results): hides the
+// launch and the block's set-up behind the predecessor's end.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                           Args&&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // The keys of a one-token row in a window or shared-prefix call, walked as whole
 // pages back to back: the pages of the sinks that lie before the window, then
 // those from the first window key on. Slot v of the walk is key v below
@@ -182,7 +212,7 @@ bool decode_side_applies(const PrefillArgs& a);
 int launch_separate_merge(const PrefillArgs& a, cudaStream_t stream);
 // Window and shared-prefix calls: the schedule, the packed kernel over its work
 // list, the decode partials (*parts: partials per split) and their merge.
-int launch_range_schedule(const PrefillArgs& a, Unit* units, Unit* units_sorted, int32_t* header, int32_t* row_ok,
+int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header, int32_t* row_ok,
                           int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
                           int64_t max_units, cudaStream_t stream);
 int launch_packed(const PrefillArgs& a, cudaStream_t stream);

@@ -25,15 +25,24 @@ struct RangeLayout {
     int32_t slots, chunk, max_splits, nparts;
 };
 
-// Keys per decode split: enough splits to give every SM two items where the
-// rows alone do not, no split shorter than 256 keys nor longer than kDecodeChunk.
+// Keys per decode split (a multiple of 128, at most kDecodeChunk): the length with
+// the shortest modelled time for rows of max_len slots. An SM takes its share of
+// the items one after the other; an item costs about 2.5 tiles of start-up on
+// top of its 128-key tiles, and every split one more partial to merge.
 int32_t decode_chunk(int32_t num_rows, int32_t hkv, int64_t max_len) {
     const int64_t items = (int64_t)num_rows * hkv;
-    const int64_t want = (2 * kSms + items - 1) / (items > 0 ? items : 1);
-    int64_t c = (max_len + want - 1) / want;
-    c = (c + kBlockN - 1) / kBlockN * kBlockN;
-    if (c < 256) c = 256;
-    return (int32_t)(c > kDecodeChunk ? kDecodeChunk : c);
+    double best = 0;
+    int32_t best_chunk = kDecodeChunk;
+    for (int32_t c = kDecodeChunk; c >= kBlockN; c -= kBlockN) {
+        const int64_t splits = (max_len + c - 1) / c;
+        const int64_t tiles = ((max_len < c ? max_len : c) + kBlockN - 1) / kBlockN;
+        const double t = (double)((items * splits + kSms - 1) / kSms) * (2.5 + (double)tiles) + 0.3 * (double)splits;
+        if (c == kDecodeChunk || t < best) {
+            best = t;
+            best_chunk = c;
+        }
+    }
+    return best_chunk;
 }
 
 // Shards of each prefix: the count with the shortest modelled time. An SM takes
@@ -83,8 +92,8 @@ RangeLayout range_layout(int32_t num_rows, int32_t num_prefixes, int32_t total_q
     w.row_grp = take((size_t)num_rows * 4);
     w.grp_shards = take((size_t)ng * 4);
     w.dec_pre = take((2 * (size_t)num_rows + 1) * 4);
-    w.units = take((size_t)w.max_units * sizeof(Unit));
-    w.units_sorted = take((size_t)w.max_units * sizeof(Unit));
+    w.units = take((size_t)w.max_units * sizeof(PackedUnit));
+    w.units_sorted = take((size_t)w.max_units * sizeof(PackedUnit));
     w.part_out = take((size_t)w.nparts * total_q * hq * d * 4);
     w.part_lse = take((size_t)w.nparts * total_q * hq * 4);
     const size_t dec = (size_t)num_rows * hq * 2 * w.max_splits;
@@ -181,7 +190,7 @@ int range_call(const RangeCall& c) {
     a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
     a.nparts = w.nparts;
     a.row_ok = ints(w.row_ok);
-    a.units = reinterpret_cast<const Unit*>(ws + w.units_sorted);
+    a.packed = reinterpret_cast<const PackedUnit*>(ws + w.units_sorted);
     a.num_units = ints(w.header);
     a.dec_pre = ints(w.dec_pre);
     a.status = c.status;
@@ -195,7 +204,8 @@ int range_call(const RangeCall& c) {
     a.prefixes = c.prefixes;
     a.num_prefixes = shared ? c.num_prefixes : 0;
 
-    int rc = launch_range_schedule(a, reinterpret_cast<Unit*>(ws + w.units), reinterpret_cast<Unit*>(ws + w.units_sorted),
+    int rc = launch_range_schedule(a, reinterpret_cast<PackedUnit*>(ws + w.units),
+                                   reinterpret_cast<PackedUnit*>(ws + w.units_sorted),
                                    ints(w.header), ints(w.row_ok), ints(w.row_lo), ints(w.row_grp),
                                    ints(w.grp_shards), ints(w.dec_pre), w.max_units, c.stream);
     if (rc != PCP_OK) return rc;
