@@ -452,21 +452,27 @@ __global__ void __launch_bounds__(256)
 // of a group also those of the prefix's shards (partials 0 .. shards - 1). A
 // longer row outside every group was written by the packed kernel.
 //
-// One warp per (token, head): lane l holds D / 32 dims. The partials are taken in
+// One warp per (token, head), the token's row found through tok_row; without
+// prefixes only rows of one token have partials, and a warp takes a (row, head).
+// Lane l holds D / 32 dims. The partials are taken in
 // batches of kMergeBatch whose loads (lse and values together) are all in flight at
 // once; a running maximum joins the batches.
 constexpr int kMergeBatch = 8;
 template <int D>
 __global__ void __launch_bounds__(256)
     range_merge_kernel(PrefillArgs a, const int32_t* __restrict__ row_grp, const int32_t* __restrict__ grp_shards,
-                       const float* __restrict__ dec_out, const float* __restrict__ dec_lse, int max_splits,
+                       const int32_t* __restrict__ tok_row, const float* __restrict__ dec_out, const float* __restrict__ dec_lse, int max_splits,
                        int parts_per_split) {
     constexpr int kV = D / 32;
     using Vec = typename std::conditional<kV == 4, float4, float2>::type;
     grid_wait();
-    const int ri = blockIdx.x, lane = threadIdx.x % 32;
-    const int h = blockIdx.y * 8 + threadIdx.x / 32;
-    if (h >= a.hq || !a.row_ok[ri]) return;
+    const int lane = threadIdx.x % 32;
+    const int64_t task = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    const int32_t at = (int32_t)(task / a.hq), h = (int32_t)(task - (int64_t)at * a.hq);
+    const bool by_token = a.num_prefixes > 0;
+    if (at >= (by_token ? a.total_q : a.num_rows)) return;
+    const int32_t ri = by_token ? tok_row[at] : at;
+    if (ri < 0 || !a.row_ok[ri]) return;
     const pcp_row_t row = a.rows[ri];
     const int32_t grp = row_grp[ri];
     if (row.q_len > 1 && grp < 0) return;
@@ -476,54 +482,52 @@ __global__ void __launch_bounds__(256)
     const int n = one ? parts_per_split * ((key_range(a, row, a.row_lo[ri]).len + a.chunk - 1) / a.chunk) : 1;
     const size_t base = ((size_t)ri * a.hq + h) * (2 * max_splits);
     const size_t out_stride = (size_t)a.total_q * a.hq * D, lse_stride = (size_t)a.hq * a.total_q;
-    // tokens of a longer row are dealt over gridDim.z
-    for (int32_t t = row.q_start + blockIdx.z; t < row.q_start + row.q_len; t += gridDim.z) {
-        const size_t li = (size_t)h * a.total_q + t, o = ((size_t)t * a.hq + h) * D;
-        float M = -INFINITY, W = 0.f, O[kV] = {};
-        for (int s0 = 0; s0 < n + shards; s0 += kMergeBatch) {
-            float ls[kMergeBatch];
-            Vec x[kMergeBatch];
+    const int32_t t = by_token ? at : row.q_start;
+    const size_t li = (size_t)h * a.total_q + t, o = ((size_t)t * a.hq + h) * D;
+    float M = -INFINITY, W = 0.f, O[kV] = {};
+    for (int s0 = 0; s0 < n + shards; s0 += kMergeBatch) {
+        float ls[kMergeBatch];
+        Vec x[kMergeBatch];
 #pragma unroll
-            for (int k = 0; k < kMergeBatch; ++k) {
-                const int s = s0 + k;
-                ls[k] = -INFINITY;
-                if (s >= n + shards) continue;
-                if (one && s < n) {
-                    ls[k] = __ldcg(dec_lse + base + s);
-                    x[k] = __ldcg(reinterpret_cast<const Vec*>(dec_out + (base + s) * D) + lane);
-                } else {
-                    const size_t p = s < n ? a.nparts - 1 : s - n;
-                    ls[k] = __ldcg(a.part_lse + p * lse_stride + li);
-                    x[k] = __ldcg(reinterpret_cast<const Vec*>(a.part_out + p * out_stride + o) + lane);
-                }
-            }
-            float m = M;
-#pragma unroll
-            for (int k = 0; k < kMergeBatch; ++k) m = fmaxf(m, ls[k]);
-            if (m == -INFINITY) continue;
-            const float f = __expf(M - m);
-            W *= f;
-#pragma unroll
-            for (int e = 0; e < kV; ++e) O[e] *= f;
-            M = m;
-#pragma unroll
-            for (int k = 0; k < kMergeBatch; ++k) {
-                if (ls[k] == -INFINITY) continue;
-                const float w = __expf(ls[k] - M);
-                W += w;
-                const float* v = reinterpret_cast<const float*>(&x[k]);
-#pragma unroll
-                for (int e = 0; e < kV; ++e) O[e] += w * v[e];
+        for (int k = 0; k < kMergeBatch; ++k) {
+            const int s = s0 + k;
+            ls[k] = -INFINITY;
+            if (s >= n + shards) continue;
+            if (one && s < n) {
+                ls[k] = __ldcg(dec_lse + base + s);
+                x[k] = __ldcg(reinterpret_cast<const Vec*>(dec_out + (base + s) * D) + lane);
+            } else {
+                const size_t p = s < n ? a.nparts - 1 : s - n;
+                ls[k] = __ldcg(a.part_lse + p * lse_stride + li);
+                x[k] = __ldcg(reinterpret_cast<const Vec*>(a.part_out + p * out_stride + o) + lane);
             }
         }
-        const float inv = W > 0.f ? 1.f / W : 0.f;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + o) + lane * (kV / 2);
-        if constexpr (kV == 4)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
-        else
-            *dst = pack_bf16x2(O[0] * inv, O[1] * inv);
-        if (lane == 0) a.lse[li] = W > 0.f ? M + __logf(W) : -INFINITY;
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) m = fmaxf(m, ls[k]);
+        if (m == -INFINITY) continue;
+        const float f = __expf(M - m);
+        W *= f;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) O[e] *= f;
+        M = m;
+#pragma unroll
+        for (int k = 0; k < kMergeBatch; ++k) {
+            if (ls[k] == -INFINITY) continue;
+            const float w = __expf(ls[k] - M);
+            W += w;
+            const float* v = reinterpret_cast<const float*>(&x[k]);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) O[e] += w * v[e];
+        }
     }
+    const float inv = W > 0.f ? 1.f / W : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + o) + lane * (kV / 2);
+    if constexpr (kV == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
+    else
+        *dst = pack_bf16x2(O[0] * inv, O[1] * inv);
+    if (lane == 0) a.lse[li] = W > 0.f ? M + __logf(W) : -INFINITY;
 }
 
 template <int D, int GMAX, bool F8, bool RNG>
@@ -622,17 +626,16 @@ int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, in
     return launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, 0, parts);
 }
 
-int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32_t* grp_shards,
+int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32_t* grp_shards, const int32_t* tok_row,
                        const float* dec_out, const float* dec_lse, int32_t max_splits, int parts,
                        cudaStream_t stream) {
-    // longer rows have tokens for several blocks; where no row can be longer than
-    // one token (num_rows == total_q) one block per row and eight heads does
-    const dim3 grid(a.num_rows, (a.hq + 7) / 8, a.total_q > a.num_rows && a.num_prefixes > 0 ? 16 : 1);
+    const int64_t tasks = (int64_t)(a.num_prefixes > 0 ? a.total_q : a.num_rows) * a.hq;
+    const dim3 grid((unsigned)((tasks + 7) / 8));
     const cudaError_t e =
-        a.d == 64 ? launch_chained(range_merge_kernel<64>, grid, dim3(256), 0, stream, a, row_grp, grp_shards, dec_out,
-                                   dec_lse, max_splits, parts)
-                  : launch_chained(range_merge_kernel<128>, grid, dim3(256), 0, stream, a, row_grp, grp_shards, dec_out,
-                                   dec_lse, max_splits, parts);
+        a.d == 64 ? launch_chained(range_merge_kernel<64>, grid, dim3(256), 0, stream, a, row_grp, grp_shards, tok_row,
+                                   dec_out, dec_lse, max_splits, parts)
+                  : launch_chained(range_merge_kernel<128>, grid, dim3(256), 0, stream, a, row_grp, grp_shards, tok_row,
+                                   dec_out, dec_lse, max_splits, parts);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }

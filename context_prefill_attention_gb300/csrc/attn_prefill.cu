@@ -1097,73 +1097,6 @@ __device__ __forceinline__ int32_t unit_cost(const Unit& u, const pcp_row_t* row
 // Partial last splits of decode rows, bucketed by their 128-key tiles (1 .. 16).
 constexpr int kTailBuckets = kDecodeChunk / kBlockN;
 
-// units[0, n) into sorted by descending cost (key tiles), by the whole block;
-// keys: kSortCap entries of shared memory.
-template <typename U, typename Cost>
-__device__ __forceinline__ void sort_units(const U* units, U* sorted, int32_t n, unsigned long long* keys,
-                                           int32_t* warp_sums, Cost cost_of) {
-    if (n > kSortCap) {
-        // Counting sort, longest first: class c = kCostBuckets - 1 - min(cost,
-        // kCostBuckets - 1); count, exclusive scan, scatter. Units of one class
-        // land in any order (every item writes only its own outputs, so the
-        // order changes no result).
-        int32_t* cnt = reinterpret_cast<int32_t*>(keys);
-        for (int32_t i = threadIdx.x; i < kCostBuckets; i += kSchedThreads) cnt[i] = 0;
-        __syncthreads();
-        for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
-            const int32_t c = kCostBuckets - 1 - min(cost_of(units[i]), kCostBuckets - 1);
-            atomicAdd(&cnt[c], 1);
-        }
-        __syncthreads();
-        constexpr int kPer = kCostBuckets / kSchedThreads;  // consecutive classes per thread
-        int32_t local[kPer], sum = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            local[k] = cnt[threadIdx.x * kPer + k];
-            sum += local[k];
-        }
-        int32_t tot;
-        int32_t run = block_exclusive_scan(sum, warp_sums, &tot);
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            cnt[threadIdx.x * kPer + k] = run;
-            run += local[k];
-        }
-        __syncthreads();
-        for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
-            const U u = units[i];
-            const int32_t c = kCostBuckets - 1 - min(cost_of(u), kCostBuckets - 1);
-            sorted[atomicAdd(&cnt[c], 1)] = u;
-        }
-        return;
-    }
-    int32_t pow2 = 1;
-    while (pow2 < n) pow2 <<= 1;
-    for (int32_t i = threadIdx.x; i < pow2; i += kSchedThreads) {
-        unsigned long long key = ~0ull;
-        if (i < n) {
-            const int32_t cost = cost_of(units[i]);
-            key = ((unsigned long long)(0x7FFFFFFF - cost) << 32) | (unsigned)i;
-        }
-        keys[i] = key;
-    }
-    __syncthreads();
-    for (int32_t k = 2; k <= pow2; k <<= 1) {
-        for (int32_t jj = k >> 1; jj > 0; jj >>= 1) {
-            for (int32_t i = threadIdx.x; i < pow2; i += kSchedThreads) {
-                const int32_t l = i ^ jj;
-                if (l > i) {
-                    const unsigned long long x = keys[i], y = keys[l];
-                    const bool up = (i & k) == 0;
-                    if ((x > y) == up) { keys[i] = y; keys[l] = x; }
-                }
-            }
-            __syncthreads();
-        }
-    }
-    for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) sorted[i] = units[(int32_t)(keys[i] & 0xFFFFFFFFu)];
-}
-
 // Place of this thread's row among the rows with a partial last split: after every
 // row of a longer bucket, and in row order within its bucket b (0: no such row),
 // so that the list, and with it every sum's order, is the same in every run.
@@ -1293,11 +1226,70 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
     }
     // every thread's units[] writes must be visible before any thread reads them
     __syncthreads();
-    sort_units(units, sorted, n, keys, warp_sums, [&](const Unit& u) { return unit_cost(u, rows, bs); });
+    if (n > kSortCap) {
+        // Counting sort, longest first: class c = kCostBuckets - 1 - min(cost,
+        // kCostBuckets - 1); count, exclusive scan, scatter. Units of one class
+        // land in any order (every item writes only its own outputs, so the
+        // order changes no result).
+        int32_t* cnt = reinterpret_cast<int32_t*>(keys);
+        for (int32_t i = threadIdx.x; i < kCostBuckets; i += kSchedThreads) cnt[i] = 0;
+        __syncthreads();
+        for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
+            const int32_t c = kCostBuckets - 1 - min(unit_cost(units[i], rows, bs), kCostBuckets - 1);
+            atomicAdd(&cnt[c], 1);
+        }
+        __syncthreads();
+        constexpr int kPer = kCostBuckets / kSchedThreads;  // consecutive classes per thread
+        int32_t local[kPer], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            local[k] = cnt[threadIdx.x * kPer + k];
+            sum += local[k];
+        }
+        int32_t tot;
+        int32_t run = block_exclusive_scan(sum, warp_sums, &tot);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            cnt[threadIdx.x * kPer + k] = run;
+            run += local[k];
+        }
+        __syncthreads();
+        for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
+            const Unit u = units[i];
+            const int32_t c = kCostBuckets - 1 - min(unit_cost(u, rows, bs), kCostBuckets - 1);
+            sorted[atomicAdd(&cnt[c], 1)] = u;
+        }
+        return;
+    }
+    int32_t pow2 = 1;
+    while (pow2 < n) pow2 <<= 1;
+    for (int32_t i = threadIdx.x; i < pow2; i += kSchedThreads) {
+        unsigned long long key = ~0ull;
+        if (i < n) {
+            const int32_t cost = unit_cost(units[i], rows, bs);
+            key = ((unsigned long long)(0x7FFFFFFF - cost) << 32) | (unsigned)i;
+        }
+        keys[i] = key;
+    }
+    __syncthreads();
+    for (int32_t k = 2; k <= pow2; k <<= 1) {
+        for (int32_t jj = k >> 1; jj > 0; jj >>= 1) {
+            for (int32_t i = threadIdx.x; i < pow2; i += kSchedThreads) {
+                const int32_t l = i ^ jj;
+                if (l > i) {
+                    const unsigned long long x = keys[i], y = keys[l];
+                    const bool up = (i & k) == 0;
+                    if ((x > y) == up) { keys[i] = y; keys[l] = x; }
+                }
+            }
+            __syncthreads();
+        }
+    }
+    for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) sorted[i] = units[(int32_t)(keys[i] & 0xFFFFFFFFu)];
 }
 
 // The scheduler of the window and shared-prefix calls: the row checks, the
-// packed work list (packed_item; longest first) and the decode work items, as
+// packed work list (packed_unit; longest first) and the decode work items, as
 // schedule_kernel lays them out but over each row's own keys and in splits of
 // a.chunk keys. A row of one token is a decode row whatever its flag. Window
 // calls (no prefixes): one unit per a.slots tiles of a longer row. Shared-prefix
@@ -1305,23 +1297,47 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
 // prefix (a.nparts - 1 shards of whole pages at most), write partials 1 ..
 // nparts - 1, a longer row's own keys partial nparts; a row outside every
 // group attends all its keys into the result at once. row_lo: each row's first
-// own key; row_grp: its group or -1; grp_shards: each group's shards (0: bad).
+// own key; row_grp: its group or -1; grp_shards: each group's shards (0: bad);
+// tok_row (shared-prefix calls): the row whose partials make up each token, or -1.
+//
+// One block, bound by latency: units are dealt to the threads by a search over
+// the rows' running counts (a thread per row would write a long row's units one
+// by one), and ordered by one counting pass over kCostClasses cost classes.
+constexpr int kCostClasses = kSchedThreads;
+
+// Index of the last entry of off[0, n) that is at most u (off ascending, off[0] <= u).
+__device__ __forceinline__ int32_t last_at_most(const int32_t* off, int32_t n, int32_t u) {
+    int32_t lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) / 2;
+        if (off[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
 __global__ void __launch_bounds__(kSchedThreads, 1)
     range_schedule_kernel(PrefillArgs a, PackedUnit* units, PackedUnit* sorted, int32_t* header, int32_t* row_ok,
-                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
+                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* tok_row, int32_t* dec_pre,
                           int64_t max_units) {
     __shared__ int32_t warp_sums[32];
     __shared__ int32_t tail_cnt[kTailBuckets + 1], tail_off[kTailBuckets + 1], tail_fill[kTailBuckets + 1];
     __shared__ int32_t tail_warp[kSchedThreads / 32][kTailBuckets + 1];
-    __shared__ __align__(16) unsigned long long keys[kSortCap];
+    __shared__ int32_t off[kSchedThreads];       // first unit of each row (group) of the round
+    __shared__ int32_t classes[kCostClasses];    // units per cost class, then the class's next place
     grid_launch_dependents();  // the decode kernel sets itself up meanwhile
     if (threadIdx.x <= kTailBuckets) {
         tail_cnt[threadIdx.x] = 0;
         tail_fill[threadIdx.x] = 0;
     }
+    classes[threadIdx.x] = 0;
     const int32_t num_rows = a.num_rows, bs = a.block_size, ng = a.num_prefixes;
     const int32_t span = a.slots * (kBlockM / (a.hq / a.hkv));
     const int64_t max_kv = (int64_t)a.max_blocks * bs;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    auto class_of = [](const PackedUnit& u) {
+        return kCostClasses - 1 - min((u.k_end + kBlockN - 1) / kBlockN, kCostClasses - 1);
+    };
     // groups: fields in range, and the tokens after those of every earlier group
     for (int32_t g = threadIdx.x; g < ng; g += kSchedThreads) {
         const pcp_prefix_t p = a.prefixes[g];
@@ -1334,14 +1350,16 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         if (!ok) report_status(a.status, PCP_ERR_RANGE);
         grp_shards[g] = ok ? min(a.nparts - 1, (p.prefix_len + kBlockN - 1) / kBlockN) : 0;
     }
+    if (ng > 0)
+        for (int32_t t = threadIdx.x; t < a.total_q; t += kSchedThreads) tok_row[t] = -1;
     __syncthreads();
     int32_t base = 0, dbase = 0;
     for (int32_t r0 = 0; r0 < num_rows; r0 += kSchedThreads) {
         const int32_t ri = r0 + threadIdx.x;
-        pcp_row_t row{};
-        int32_t cnt = 0, dcnt = 0, lo = 0, grp = -1;
+        int32_t cnt = 0, dcnt = 0;
         if (ri < num_rows) {
-            row = a.rows[ri];
+            const pcp_row_t row = a.rows[ri];
+            int32_t lo = 0, grp = -1;
             // (without prefixes the packed kernel is not launched for num_rows >= total_q)
             bool ok = row_in_range(row, a.num_reqs, a.total_q, max_kv) &&
                       (row.q_len == 1 || ng > 0 || a.total_q > num_rows);
@@ -1369,6 +1387,7 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
                 dcnt = (nv / a.chunk) * a.hkv;
                 const int32_t part = nv % a.chunk;
                 if (part) atomicAdd(&tail_cnt[(part + kBlockN - 1) / kBlockN], 1);
+                if (ng > 0) tok_row[row.q_start] = ri;
             }
         }
         int32_t dtot;
@@ -1376,39 +1395,51 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         if (ri < num_rows) dec_pre[ri] = doff;
         dbase += dtot;
         int32_t tot;
-        const int32_t off = base + block_exclusive_scan(cnt, warp_sums, &tot);
-        for (int32_t u = 0; u < cnt; ++u) {
-            if (off + u >= max_units) break;
-            units[off + u] = packed_unit(a, row.req, row.q_start, row.q_len, row.kv_end - row.q_len, u, span, lo,
-                                         row.kv_end, grp >= 0 ? a.nparts : 0);
+        off[threadIdx.x] = block_exclusive_scan(cnt, warp_sums, &tot);
+        __syncthreads();
+        for (int32_t u = threadIdx.x; u < tot && base + u < max_units; u += kSchedThreads) {
+            const int32_t i = last_at_most(off, kSchedThreads, u);
+            const pcp_row_t row = a.rows[r0 + i];
+            const PackedUnit x = packed_unit(a, row.req, row.q_start, row.q_len, row.kv_end - row.q_len, u - off[i], span,
+                                             row_lo[r0 + i], row.kv_end, row_grp[r0 + i] >= 0 ? a.nparts : 0);
+            units[base + u] = x;
+            atomicAdd(&classes[class_of(x)], 1);
         }
+        if (ng > 0)  // a warp per unit
+            for (int32_t u = warp; u < tot; u += kSchedThreads / 32) {
+                const int32_t i = last_at_most(off, kSchedThreads, u);
+                if (row_grp[r0 + i] < 0) continue;
+                const pcp_row_t row = a.rows[r0 + i];
+                const int32_t t1 = min(row.q_len, (u - off[i] + 1) * span);
+                for (int32_t t = (u - off[i]) * span + lane; t < t1; t += 32) tok_row[row.q_start + t] = r0 + i;
+            }
         base += tot;
+        __syncthreads();  // off is rewritten
     }
     for (int32_t g0 = 0; g0 < ng; g0 += kSchedThreads) {
         const int32_t g = g0 + threadIdx.x;
-        int32_t cnt = 0, shards = 0;
-        pcp_prefix_t p{};
-        if (g < ng) {
-            p = a.prefixes[g];
-            shards = grp_shards[g];
-            cnt = shards * ((p.q_len + span - 1) / span);
-        }
+        int32_t cnt = 0;
+        if (g < ng) cnt = grp_shards[g] * ((a.prefixes[g].q_len + span - 1) / span);
         int32_t tot;
-        const int32_t off = base + block_exclusive_scan(cnt, warp_sums, &tot);
-        const int32_t pages = (p.prefix_len + bs - 1) / bs;
-        for (int32_t u = 0; u < cnt; ++u) {
-            if (off + u >= max_units) break;
-            const int32_t sh = u % shards;
+        off[threadIdx.x] = block_exclusive_scan(cnt, warp_sums, &tot);
+        __syncthreads();
+        for (int32_t u = threadIdx.x; u < tot && base + u < max_units; u += kSchedThreads) {
+            const int32_t i = last_at_most(off, kSchedThreads, u);
+            const pcp_prefix_t p = a.prefixes[g0 + i];
+            const int32_t shards = grp_shards[g0 + i], pages = (p.prefix_len + bs - 1) / bs;
+            const int32_t sh = (u - off[i]) % shards, mt = (u - off[i]) / shards;
             const int32_t k_lo = (int32_t)((int64_t)pages * sh / shards) * bs;
             const int32_t k_hi = (int32_t)min((int64_t)p.prefix_len, (int64_t)pages * (sh + 1) / shards * bs);
-            PackedUnit x = packed_unit(a, p.req, p.q_start, p.q_len, 0, u / shards, span, k_lo, k_hi, 1 + sh);
+            PackedUnit x = packed_unit(a, p.req, p.q_start, p.q_len, 0, mt, span, k_lo, k_hi, 1 + sh);
             x.pos0 = k_hi;  // every query lies past the prefix
             x.k_lo = k_lo;
             x.shift = k_lo;
             x.k_end = k_hi - k_lo;
-            units[off + u] = x;
+            units[base + u] = x;
+            atomicAdd(&classes[class_of(x)], 1);
         }
         base += tot;
+        __syncthreads();
     }
     const int32_t n = (int32_t)min((int64_t)base, max_units);
     __syncthreads();
@@ -1434,9 +1465,17 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         const int32_t at = tail_place(b, tail_off, tail_fill, tail_warp);
         if (b) dec_pre[num_rows + 1 + at] = ri;
     }
-    if (n > 0)
-        sort_units(units, sorted, n, keys, warp_sums,
-                   [&](const PackedUnit& u) { return (u.k_end + kBlockN - 1) / kBlockN; });
+    if (n == 0) return;
+    // longest first (units of one class in any order: an item writes only its own
+    // results, which do not depend on its place)
+    int32_t tot;
+    const int32_t first = block_exclusive_scan(classes[threadIdx.x], warp_sums, &tot);
+    classes[threadIdx.x] = first;
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
+        const PackedUnit x = units[i];
+        sorted[atomicAdd(&classes[class_of(x)], 1)] = x;
+    }
 }
 
 // ---------------------------------------------------------------- tensor maps
@@ -1538,11 +1577,11 @@ int launch_schedule(const PrefillArgs& a, int32_t flags, Unit* units, Unit* unit
     return PCP_OK;
 }
 
-int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header, int32_t* row_ok,
-                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
-                          int64_t max_units, cudaStream_t stream) {
+int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header,
+                          int32_t* row_ok, int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* tok_row,
+                          int32_t* dec_pre, int64_t max_units, cudaStream_t stream) {
     range_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(a, units, units_sorted, header, row_ok, row_lo, row_grp,
-                                                           grp_shards, dec_pre, max_units);
+                                                           grp_shards, tok_row, dec_pre, max_units);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;

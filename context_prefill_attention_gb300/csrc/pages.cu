@@ -24,7 +24,7 @@ namespace pcp {
 namespace {
 
 constexpr int kPageThreads = 256;
-constexpr int kPer = 16;                          // ids per thread of a chunk
+constexpr int kPer = 4;                           // ids per thread of a chunk
 constexpr int kChunk = kPageThreads * kPer;       // ids per counting block
 constexpr int kCopyThreads = 512;
 constexpr int kCopyUnroll = 4;                    // 16-byte loads in flight per thread
@@ -106,11 +106,19 @@ __global__ void __launch_bounds__(kPageThreads)
     __shared__ int32_t warp_sums[kPageThreads / 32];
     const int64_t base = (int64_t)blockIdx.x * kChunk;
     int32_t n = 0;
-    for (int i = threadIdx.x; i < kChunk; i += kPageThreads) {
-        if (base + i >= num_blocks) break;
-        const int32_t r = ref[base + i];
-        if (ref_out) ref_out[base + i] = r;
-        n += (r > 0) != kFree;
+    grid_launch_dependents();
+    int32_t r[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int64_t i = base + e * kPageThreads + threadIdx.x;
+        r[e] = i < num_blocks ? ref[i] : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+        const int64_t i = base + e * kPageThreads + threadIdx.x;
+        if (i >= num_blocks) continue;
+        if (ref_out) ref_out[i] = r[e];
+        n += (r[e] > 0) != kFree;
     }
     n = block_sum(n, warp_sums);
     if (threadIdx.x == 0) counts[blockIdx.x] = n;
@@ -124,6 +132,7 @@ __global__ void __launch_bounds__(kPageThreads)
                 int32_t* ref_out, const int32_t* __restrict__ counts, int32_t chunks, int32_t* status) {
     __shared__ int32_t warp_sums[kPageThreads / 32];
     __shared__ int32_t found;
+    grid_wait();
     const int32_t child = blockIdx.x;
     // tokens of child j: its parent's, 0 where it has none or a bad one
     auto tokens_of = [&](int32_t j) -> int32_t {
@@ -209,12 +218,21 @@ __global__ void __launch_bounds__(kPageThreads)
     }
 }
 
+// ref_out = ref.
+__global__ void __launch_bounds__(kPageThreads)
+    copy_counts_kernel(const int32_t* __restrict__ ref, int32_t* __restrict__ ref_out, int64_t num_blocks) {
+    grid_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x;
+    if (i < num_blocks) ref_out[i] = ref[i];
+}
+
 // Entries [first[r], last[r]) of every row give their reference back and become
 // -1; entries that are -1 already are passed over.
 __global__ void __launch_bounds__(kPageThreads)
     release_kernel(const int32_t* table, int32_t num_reqs, int32_t mb, const int32_t* __restrict__ first,
                    const int32_t* __restrict__ last, int64_t num_blocks, int32_t* table_out, int32_t* ref_out,
                    int32_t* status) {
+    grid_wait();
     const int64_t n = (int64_t)num_reqs * mb;
     for (int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kPageThreads) {
         const int32_t r = (int32_t)(i / mb), col = (int32_t)(i - (int64_t)r * mb);
@@ -243,6 +261,8 @@ __global__ void __launch_bounds__(kPageThreads)
                       int32_t chunks, int32_t* __restrict__ ref_out, int32_t* __restrict__ holes,
                       int32_t* __restrict__ movers, int32_t* __restrict__ rank, int32_t* header, int32_t* num_live) {
     __shared__ int32_t warp_sums[kPageThreads / 32];
+    grid_launch_dependents();
+    grid_wait();
     int32_t total = 0, before = 0;
     for (int32_t c = threadIdx.x; c < chunks; c += kPageThreads) {
         const int32_t n = counts[c];
@@ -290,6 +310,7 @@ __global__ void __launch_bounds__(kCopyThreads)
                       const int32_t* __restrict__ rank, const int32_t* __restrict__ header,
                       const int32_t* __restrict__ table, int64_t entries, int32_t* __restrict__ table_out,
                       int32_t* __restrict__ ref_out, int32_t* status) {
+    grid_wait();
     const int32_t n_live = header[0], moves = header[1];
     const int64_t tid = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x, step = (int64_t)gridDim.x * kCopyThreads;
     for (int64_t i = tid; i < entries; i += step) {
@@ -323,8 +344,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     }
 }
 
-int launched() {
-    const cudaError_t e = cudaGetLastError();
+int launched(cudaError_t e) {
     if (e != cudaSuccess) {
         set_last_cuda_error(e);
         return PCP_ERR_CUDA;
@@ -390,13 +410,12 @@ extern "C" int pcp_kv_fork(void* key_cache, void* value_cache, int64_t num_block
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int32_t* counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.counts);
     count_kernel<true><<<w.chunks, kPageThreads, 0, s>>>(ref_count, ref_count_out, num_blocks, counts);
-    int e = launched();
+    const int e = launched(cudaGetLastError());
     if (e != PCP_OK || num_children == 0) return e;
-    fork_kernel<<<num_children, kPageThreads, 0, s>>>(
-        static_cast<uint4*>(key_cache), static_cast<uint4*>(value_cache), num_blocks, block_size, slot_bytes / 16,
-        block_table, num_reqs, max_blocks_per_req, kv_len, parent, ref_count, block_table_out, ref_count_out, counts,
-        w.chunks, status);
-    return launched();
+    return launched(launch_chained(fork_kernel, dim3(num_children), dim3(kPageThreads), 0, s,
+                                   static_cast<uint4*>(key_cache), static_cast<uint4*>(value_cache), num_blocks,
+                                   block_size, slot_bytes / 16, block_table, num_reqs, max_blocks_per_req, kv_len,
+                                   parent, ref_count, block_table_out, ref_count_out, counts, w.chunks, status));
 }
 
 extern "C" int pcp_kv_release(const int32_t* block_table, int32_t num_reqs, int32_t max_blocks_per_req,
@@ -420,21 +439,26 @@ extern "C" int pcp_kv_release(const int32_t* block_table, int32_t num_reqs, int3
         overlaps_any(table_out, ranges, 2) || overlaps_any(ref_out, ranges, 2))
         return PCP_ERR_ARG;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (ref_count != ref_count_out && num_blocks > 0) {
-        const cudaError_t e = cudaMemcpyAsync(ref_count_out, ref_count, ref.n, cudaMemcpyDeviceToDevice, s);
-        if (e != cudaSuccess) {
-            set_last_cuda_error(e);
-            return PCP_ERR_CUDA;
-        }
+    const bool copy = ref_count != ref_count_out && num_blocks > 0;
+    if (copy) {
+        copy_counts_kernel<<<(unsigned)((num_blocks + kPageThreads - 1) / kPageThreads), kPageThreads, 0, s>>>(
+            ref_count, ref_count_out, num_blocks);
+        const int e = launched(cudaGetLastError());
+        if (e != PCP_OK) return e;
     }
     if (entries == 0) return PCP_OK;
     int64_t blocks = (entries + kPageThreads - 1) / kPageThreads;
     const int64_t cap = (int64_t)num_sms() * 8;
     if (blocks > cap) blocks = cap;
-    release_kernel<<<(unsigned)blocks, kPageThreads, 0, s>>>(block_table, num_reqs, max_blocks_per_req, first_page,
-                                                             last_page, num_blocks, block_table_out, ref_count_out,
-                                                             status);
-    return launched();
+    if (!copy) {  // nothing of this call to be chained behind
+        release_kernel<<<(unsigned)blocks, kPageThreads, 0, s>>>(block_table, num_reqs, max_blocks_per_req, first_page,
+                                                                 last_page, num_blocks, block_table_out,
+                                                                 ref_count_out, status);
+        return launched(cudaGetLastError());
+    }
+    return launched(launch_chained(release_kernel, dim3((unsigned)blocks), dim3(kPageThreads), 0, s, block_table,
+                                   num_reqs, max_blocks_per_req, first_page, last_page, num_blocks, block_table_out,
+                                   ref_count_out, status));
 }
 
 extern "C" int pcp_kv_compact(void* key_cache, void* value_cache, int64_t num_blocks, int32_t block_size,
@@ -468,16 +492,15 @@ extern "C" int pcp_kv_compact(void* key_cache, void* value_cache, int64_t num_bl
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
     count_kernel<false><<<w.chunks, kPageThreads, 0, s>>>(ref_count, nullptr, num_blocks, ints(w.counts));
-    int e = launched();
+    int e = launched(cudaGetLastError());
     if (e != PCP_OK) return e;
-    plan_moves_kernel<<<w.chunks, kPageThreads, 0, s>>>(ref_count, num_blocks, ints(w.counts), w.chunks, ref_count_out,
-                                                        ints(w.holes), ints(w.movers), ints(w.rank), ints(w.header),
-                                                        num_live);
-    e = launched();
+    e = launched(launch_chained(plan_moves_kernel, dim3(w.chunks), dim3(kPageThreads), 0, s, ref_count, num_blocks,
+                                ints(w.counts), w.chunks, ref_count_out, ints(w.holes), ints(w.movers), ints(w.rank),
+                                ints(w.header), num_live));
     if (e != PCP_OK) return e;
-    move_pages_kernel<<<num_sms() * 4, kCopyThreads, 0, s>>>(
-        static_cast<uint4*>(key_cache), static_cast<uint4*>(value_cache), block_size * (slot_bytes / 16), ref_count,
-        num_blocks, ints(w.holes), ints(w.movers), ints(w.rank), ints(w.header), block_table, entries, block_table_out,
-        ref_count_out, status);
-    return launched();
+    return launched(launch_chained(move_pages_kernel, dim3(num_sms() * 4), dim3(kCopyThreads), 0, s,
+                                   static_cast<uint4*>(key_cache), static_cast<uint4*>(value_cache),
+                                   block_size * (slot_bytes / 16), ref_count, num_blocks, ints(w.holes),
+                                   ints(w.movers), ints(w.rank), ints(w.header), block_table, entries,
+                                   block_table_out, ref_count_out, status));
 }

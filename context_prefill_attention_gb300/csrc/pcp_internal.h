@@ -212,13 +212,13 @@ bool decode_side_applies(const PrefillArgs& a);
 int launch_separate_merge(const PrefillArgs& a, cudaStream_t stream);
 // Window and shared-prefix calls: the schedule, the packed kernel over its work
 // list, the decode partials (*parts: partials per split) and their merge.
-int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header, int32_t* row_ok,
-                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* dec_pre,
-                          int64_t max_units, cudaStream_t stream);
+int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header,
+                          int32_t* row_ok, int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* tok_row,
+                          int32_t* dec_pre, int64_t max_units, cudaStream_t stream);
 int launch_packed(const PrefillArgs& a, cudaStream_t stream);
 int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, int* parts,
                         cudaStream_t stream);
-int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32_t* grp_shards,
+int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32_t* grp_shards, const int32_t* tok_row,
                        const float* dec_out, const float* dec_lse, int32_t max_splits, int parts,
                        cudaStream_t stream);
 int launch_cache_write(const void* k, const void* v, const int64_t* slot, int32_t num_tokens,

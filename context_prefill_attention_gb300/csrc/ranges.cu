@@ -19,7 +19,7 @@ constexpr int kMaxPrefixes = 1024;
 constexpr int kMaxShards = 32;     // shards of a prefix
 
 struct RangeLayout {
-    size_t header, row_ok, row_lo, row_grp, grp_shards, dec_pre, units, units_sorted, part_out, part_lse, dec_out,
+    size_t header, row_ok, row_lo, row_grp, grp_shards, tok_row, dec_pre, units, units_sorted, part_out, part_lse, dec_out,
         dec_lse, total;
     int64_t max_units;
     int32_t slots, chunk, max_splits, nparts;
@@ -91,6 +91,7 @@ RangeLayout range_layout(int32_t num_rows, int32_t num_prefixes, int32_t total_q
     w.row_lo = take((size_t)num_rows * 4);
     w.row_grp = take((size_t)num_rows * 4);
     w.grp_shards = take((size_t)ng * 4);
+    w.tok_row = take(ng > 0 ? (size_t)total_q * 4 : 0);
     w.dec_pre = take((2 * (size_t)num_rows + 1) * 4);
     w.units = take((size_t)w.max_units * sizeof(PackedUnit));
     w.units_sorted = take((size_t)w.max_units * sizeof(PackedUnit));
@@ -207,7 +208,7 @@ int range_call(const RangeCall& c) {
     int rc = launch_range_schedule(a, reinterpret_cast<PackedUnit*>(ws + w.units),
                                    reinterpret_cast<PackedUnit*>(ws + w.units_sorted),
                                    ints(w.header), ints(w.row_ok), ints(w.row_lo), ints(w.row_grp),
-                                   ints(w.grp_shards), ints(w.dec_pre), w.max_units, c.stream);
+                                   ints(w.grp_shards), ints(w.tok_row), ints(w.dec_pre), w.max_units, c.stream);
     if (rc != PCP_OK) return rc;
     float* dec_out = reinterpret_cast<float*>(ws + w.dec_out);
     float* dec_lse = reinterpret_cast<float*>(ws + w.dec_lse);
@@ -220,7 +221,8 @@ int range_call(const RangeCall& c) {
         rc = launch_packed(a, c.stream);
         if (rc != PCP_OK) return rc;
     }
-    return launch_range_merge(a, ints(w.row_grp), ints(w.grp_shards), dec_out, dec_lse, w.max_splits, parts, c.stream);
+    return launch_range_merge(a, ints(w.row_grp), ints(w.grp_shards), ints(w.tok_row), dec_out, dec_lse, w.max_splits,
+                              parts, c.stream);
 }
 
 bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
