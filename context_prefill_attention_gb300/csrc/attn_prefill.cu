@@ -211,7 +211,7 @@ __device__ __forceinline__ PackedUnit packed_unit(const PrefillArgs& a, int32_t 
 __device__ __forceinline__ Item packed_item(const PrefillArgs& a, int32_t idx) {
     const int32_t n = idx / a.hkv;
     const int4* src = reinterpret_cast<const int4*>(a.packed + n);
-    const int4 x = __ldcg(src), y = __ldcg(src + 1);
+    const int4 x = src[0], y = src[1];
     Item it{};
     it.nslots = a.slots;
     it.hk = idx - n * a.hkv;
@@ -424,6 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // issuer reads one barrier per tile for both (every barrier read by the issuer
     // costs tensor-pipe time); FP8: the converters fill k_full and v_full apart
     constexpr bool kMerged = !F8;
+    // arrivals that free a K or V stage: one thread's, or (PACK) one of each of the
+    // four warps that held results in it, else one thread's for all four
+    constexpr uint32_t kRel = PACK ? 4 : 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
 
@@ -446,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // FP8: a stage is full when both converter warps have arrived
         const uint32_t fill_count = F8 ? kConvThreads / 32 : 1;
         // (FP8, D = 128: the K codes are the MMA operand, full once TMA has landed them)
-        for (int s = 0; s < kNK; ++s) { mbar_init(k_full(s), C::kE4 ? 1 : fill_count); mbar_init(k_empty(s), 1); }
-        for (int s = 0; s < kNV; ++s) { mbar_init(v_full(s), fill_count); mbar_init(v_empty(s), 1); }
+        for (int s = 0; s < kNK; ++s) { mbar_init(k_full(s), C::kE4 ? 1 : fill_count); mbar_init(k_empty(s), kRel); }
+        for (int s = 0; s < kNV; ++s) { mbar_init(v_full(s), fill_count); mbar_init(v_empty(s), kRel); }
         if (F8) {
             for (int s = 0; s < kNK; ++s) mbar_init(kc_full(s), 1);
             for (int s = 0; s < kNV; ++s) mbar_init(vc_full(s), 1);
@@ -734,13 +737,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t t_s = tmem + lane_base + C::tmem_s(g);
         const uint32_t t_o = tmem + lane_base + C::tmem_o(g);
-        uint32_t sph = 0, oph = 0;
         // The warpgroup of the last head slot releases the shared stages: S of tile j
         // complete means every MMA issued before it is complete (K(j), V(j - 1) and,
         // on the last tile, Q are free); O done frees the item's last V. Its thread 0
         // arrives, so that the MMA issuer spends no commits on them.
         const bool releaser = g == slots_per_item - 1;
-        uint32_t rel_k = 0, rel_v = 0, cq = 0, vt_all = 0;
+        uint32_t kt = 0, cq = 0;  // tiles and items (with tiles) so far: stages and phases follow from them
         bool ok = true;
         for (int32_t round = 0; ok; ++round) {
             const int32_t idx = item_of_round(round);
@@ -764,8 +766,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t full_hi = PACK ? min(it.k_hi, it.pos0 + 1) - it.shift : 0;
             float m = -INFINITY, l = 0.f;
             const int n = it.n_tiles;
-            const uint32_t vt0 = vt_all;  // tiles before this item: V(j) is in stage (vt0 + j) % kNV
-            vt_all += n;
             // FP8, D = 128: once the item's bf16 Q has landed, this thread rewrites its
             // own row as e4m3 terms (the softmax warps are idle until the item's first S)
             // and keeps the row's q scale
@@ -781,16 +781,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if ((threadIdx.x & 31) == 0) mbar_arrive(q_full);
                 }
             }
-            for (int j = 0; j < n && ok; ++j) {
-                if (!(ok = mbar_wait_warp(s_full(g), sph, abort_flag))) break;
-                sph ^= 1;
-                if (releaser) {
-                    if (r == 0) {
-                        mbar_arrive(k_empty(rel_k % kNK));
-                        if (j > 0) mbar_arrive(v_empty(rel_v % kNV));
-                    }
-                    ++rel_k;
-                    if (j > 0) ++rel_v;
+            for (int j = 0; j < n && ok; ++j, ++kt) {
+                if (!(ok = mbar_wait_warp(s_full(g), kt & 1, abort_flag))) break;
+                if (releaser && r == 0) {
+                    // PACK: the last K stage is still to hold head slot 0's results
+                    if (!PACK || j + 1 < n) mbar_arrive_n(k_empty(kt % kNK), kRel);
+                    if (j > 0) mbar_arrive_n(v_empty((kt - 1) % kNV), kRel);
                 }
                 if (j == n - 1 && (releaser || dual) && r == 0) mbar_arrive(q_empty);
                 tc_fence_after();
@@ -800,21 +796,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t key0 = PACK ? j * kBlockN : it.kb + j * kBlockN;
                 const bool full = PACK ? key0 >= full_lo && key0 + kBlockN <= full_hi
                                        : key0 >= it.k_lo && key0 + kBlockN <= it.k_hi && key0 + kBlockN - 1 <= it.pos0;
-                // keys outside [k_lo, min(k_hi, pos + 1)) of the tile's columns [c0, 128) at -inf.
-                // PACK: in slots, the row's own window and the sinks; its bounds are read again
-                // here, in the few tiles that need them, rather than held in registers
+                // keys outside [k_lo, min(k_hi, pos + 1)) of the tile's columns [c0, 128) at -inf
                 auto mask_scores = [&](float* x, auto c0) {
-                    int32_t lo = it.k_lo - key0, hi = min(it.k_hi, pos + 1) - key0, sk = 0;
-                    if constexpr (PACK) {
+                    if constexpr (!PACK) {
+                        const int32_t lo = it.k_lo - key0;
+                        const int32_t hi = min(it.k_hi, pos + 1) - key0;
+#pragma unroll
+                        for (int c2 = decltype(c0)::value; c2 < 128; ++c2)
+                            if (c2 < lo || c2 >= hi) x[c2] = -INFINITY;
+                    } else {
+                        // in slots, the row's own window and the sinks; the unit is read again here
+                        // (an L1 hit), in the few tiles that need it, rather than held in registers.
+                        // A warp's rows are few tokens, so its edges fall into one or two of the
+                        // four 32-column parts: a part that every row sees whole is passed over,
+                        // the others take a bit per column (measured at 1024 keys, 9 tiles per
+                        // item: a compare of every column cost 5 us of the item's 24.7)
                         const Item m_it = item_at(idx);
                         const int32_t m_pos = m_it.pos0 + min(g * tpt + r / G, m_it.rows_valid - 1);
-                        lo = max(m_it.k_lo, m_pos - a.window + 1) - m_it.shift - key0;
-                        hi = min(m_it.k_hi, m_pos + 1) - m_it.shift - key0;
-                        sk = a.sinks - key0;
-                    }
+                        const int32_t lo = max(m_it.k_lo, m_pos - a.window + 1) - m_it.shift - key0;
+                        const int32_t hi = min(m_it.k_hi, m_pos + 1) - m_it.shift - key0;
+                        const int32_t lo_max = __reduce_max_sync(0xffffffffu, lo);
+                        const int32_t hi_min = __reduce_min_sync(0xffffffffu, hi);
+                        auto below = [](int32_t n) -> uint32_t {
+                            return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
+                        };
 #pragma unroll
-                    for (int c2 = decltype(c0)::value; c2 < 128; ++c2)
-                        if ((c2 < lo && (!PACK || c2 >= sk)) || c2 >= hi) x[c2] = -INFINITY;
+                        for (int p0 = decltype(c0)::value; p0 < 128; p0 += 32) {
+                            if (p0 >= lo_max && p0 + 32 <= hi_min) continue;
+                            const uint32_t seen =
+                                below(hi - p0) & (~below(lo - p0) | below(a.sinks - key0 - p0));
+#pragma unroll
+                            for (int c2 = 0; c2 < 32; ++c2)
+                                if (!(seen & (1u << c2))) x[p0 + c2] = -INFINITY;
+                        }
+                    }
                 };
                 // S row of this thread into registers, masked
                 auto load_scores = [&]() {
@@ -838,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // P, and with it this tile's first PV, is released; S(j) done means that
                     // V(j) has landed
                     if (g == 0 && !full && !packed_slot_live(item_at(idx), a.sinks, key0 + r)) {
-                        uint8_t* vrow = smem + C::kV + ((vt0 + j) % kNV) * C::kTileBytes + r * 128;
+                        uint8_t* vrow = smem + C::kV + (kt % kNV) * C::kTileBytes + r * 128;
 #pragma unroll
                         for (int h2 = 0; h2 < C::kHalves; ++h2)
 #pragma unroll
@@ -968,20 +983,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = has ? vd / l : 0.f;
             const float lse_v = has ? (m + __log2f(l)) * kLn2 : -INFINITY;
             if (n > 0) {
-                if (!(ok = mbar_wait_warp(o_done(g), oph, abort_flag))) break;
-                oph ^= 1;
-                if (releaser) {
-                    if (r == 0) mbar_arrive(v_empty(rel_v % kNV));
-                    ++rel_v;
-                }
+                if (!(ok = mbar_wait_warp(o_done(g), (cq - 1) & 1, abort_flag))) break;
+                // (PACK: the last V stage is still to hold head slot 1's results)
+                if (releaser && r == 0 && (!PACK || g == 0)) mbar_arrive_n(v_empty((kt - 1) % kNV), kRel);
                 tc_fence_after();
             }
-            // PACK: the unit's fields again, for the same reason
-            const Item e_it = PACK ? item_at(idx) : it;
-            const int32_t e_tl = PACK ? g * tpt + r / G : 0;
-            const int32_t e_tok = PACK ? e_it.q_tok0 + e_tl : tok, e_h = PACK ? e_it.h0 + r % G : h;
-            const bool e_valid = PACK ? r < tpt * G && e_tl < e_it.rows_valid : valid;
-            const size_t orow = ((size_t)e_tok * a.hq + e_h) * D;
+            const size_t orow = ((size_t)tok * a.hq + h) * D;
             // the whole O row into registers first, so the accumulator can be handed
             // back to the MMA warp (next item) before the global stores
             uint32_t orow_regs[D];
@@ -996,11 +1003,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < D; ++e) orow_regs[e] = 0u;
             }
+            if constexpr (PACK) {
+                // A thread's row is contiguous, but a store of 16 bytes per lane then touches
+                // 32 lines (measured: 4 us of the 24.7 us of a 1024-key item). So each warp
+                // turns its 32 rows over in shared memory, one row's width (kRowB bytes: bf16
+                // the whole row, fp32 half of it) at a time, and stores whole rows: head slot
+                // 0 in the item's last K stage, slot 1 in its last V stage, both free since
+                // the slot's last MMA is done, and released after it.
+                constexpr int kRowB = C::kTileBytes / 128, kCh = kRowB / 16;  // bytes, 16-byte chunks
+                const Item e_it = item_at(idx);  // again rather than held, as in mask_scores
+                const int32_t e_tl = g * tpt + r / G, e_tok = e_it.q_tok0 + e_tl, e_h = e_it.h0 + r % G;
+                const bool e_valid = r < tpt * G && e_tl < e_it.rows_valid;
+                const int32_t out_row = e_valid ? e_tok * a.hq + e_h : -1;
+                const int lane32 = threadIdx.x & 31;
+                uint8_t* stage = smem + (g == 0 ? C::kK + ((kt - 1) % kNK) * C::kTileBytes
+                                                : C::kV + ((kt - 1) % kNV) * C::kTileBytes) +
+                                 (r - lane32) * kRowB;
+                auto turn = [&](auto chunk, uint8_t* base, int64_t row_bytes) {
+#pragma unroll
+                    for (int c2 = 0; c2 < kCh; ++c2)
+                        *reinterpret_cast<uint4*>(stage + lane32 * kRowB + ((c2 ^ (lane32 & (kCh - 1))) << 4)) = chunk(c2);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kCh; ++i) {
+                        const int row = i * (32 / kCh) + lane32 / kCh, c2 = lane32 % kCh;
+                        const uint4 w = *reinterpret_cast<const uint4*>(stage + row * kRowB + ((c2 ^ (row & (kCh - 1))) << 4));
+                        const int32_t to = __shfl_sync(0xffffffffu, out_row, row);
+                        if (to >= 0) *reinterpret_cast<uint4*>(base + to * row_bytes + c2 * 16) = w;
+                    }
+                    __syncwarp();
+                };
+                if (n > 0) {
+                    if (e_it.pass == 0) {
+                        turn([&](int c2) {
+                            auto two = [&](int e) {
+                                return pack_bf16x2(__uint_as_float(orow_regs[8 * c2 + e]) * inv,
+                                                   __uint_as_float(orow_regs[8 * c2 + e + 1]) * inv);
+                            };
+                            return make_uint4(two(0), two(2), two(4), two(6));
+                        }, static_cast<uint8_t*>(a.out), kRowB);
+                    } else {
+                        uint8_t* part = reinterpret_cast<uint8_t*>(a.part_out + (size_t)(e_it.pass - 1) * a.total_q * a.hq * D);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            turn([&](int c2) {
+                                auto one = [&](int e) {
+                                    return __float_as_uint(__uint_as_float(orow_regs[half * (D / 2) + 4 * c2 + e]) * inv);
+                                };
+                                return make_uint4(one(0), one(1), one(2), one(3));
+                            }, part + half * kRowB, 2 * kRowB);
+                    }
+                    float* lse_dst = e_it.pass == 0 ? a.lse : a.part_lse + (size_t)(e_it.pass - 1) * a.hq * a.total_q;
+                    if (e_valid) lse_dst[(size_t)e_h * a.total_q + e_tok] = lse_v;
+                    // this warp has read its rows back: its part of the stage may be loaded again
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane32 == 0) mbar_arrive(g == 0 ? k_empty((kt - 1) % kNK) : v_empty((kt - 1) % kNV));
+                }
+                continue;
+            }
 #pragma unroll
             for (int c2 = 0; c2 < D / 32; ++c2) {
                 const uint32_t* o = &orow_regs[32 * c2];
-                if (e_valid) {
-                    if (e_it.pass == 0) {
+                if (valid) {
+                    if (it.pass == 0) {
                         uint4* dst = reinterpret_cast<uint4*>(
                             reinterpret_cast<__nv_bfloat16*>(a.out) + orow + 32 * c2);
 #pragma unroll
@@ -1014,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {
                         float4* dst = reinterpret_cast<float4*>(
-                            a.part_out + (size_t)(e_it.pass - 1) * a.total_q * a.hq * D + orow + 32 * c2);
+                            a.part_out + (size_t)(it.pass - 1) * a.total_q * a.hq * D + orow + 32 * c2);
 #pragma unroll
                         for (int v4 = 0; v4 < 8; ++v4)
                             dst[v4] = make_float4(__uint_as_float(o[4 * v4 + 0]) * inv, __uint_as_float(o[4 * v4 + 1]) * inv,
@@ -1022,9 +1088,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (e_valid) {
-                float* lse_dst = e_it.pass == 0 ? a.lse : a.part_lse + (size_t)(e_it.pass - 1) * a.hq * a.total_q;
-                lse_dst[(size_t)e_h * a.total_q + e_tok] = lse_v;
+            if (valid) {
+                float* lse_dst = it.pass == 0 ? a.lse : a.part_lse + (size_t)(it.pass - 1) * a.hq * a.total_q;
+                lse_dst[(size_t)h * a.total_q + tok] = lse_v;
             }
         }
         if (!ok) report_status(a.status, PCP_ERR_TIMEOUT);
