@@ -362,6 +362,13 @@ __global__ void __launch_bounds__(kDecThreads)
             }
         }
         const int h = hk * G + g;
+        if (RNG && a.direct) {  // every row is one split: the result itself
+            const int32_t t = row.q_start;
+            reinterpret_cast<__nv_bfloat16*>(a.out)[((size_t)t * a.hq + h) * D + d] =
+                __float2bfloat16_rn(L > 0.f ? O / L * vd : 0.f);
+            if (d == 0) a.lse[(size_t)h * a.total_q + t] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+            continue;
+        }
         const size_t slot = ((size_t)ri * a.hq + h) * (2 * max_splits) + split;  // one partial per split
         dec_out[slot * D + d] = L > 0.f ? O / L * vd : 0.f;
         if (d == 0) dec_lse[slot] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
@@ -445,62 +452,53 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Merge of a window or shared-prefix call: the results of every row that has more
-// than one partial, by log-sum-exp, into out (bf16) and lse. A row of one token
-// has parts_per_split partials for each split of its own keys; a longer row of
-// a prefix group one for its own keys (partial nparts - 1 of part_out); the rows
-// of a group also those of the prefix's shards (partials 0 .. shards - 1). A
-// longer row outside every group was written by the packed kernel.
+// Merge of a window or shared-prefix call: the results of every token that has
+// partials, by log-sum-exp, into out (bf16) and lse. A row of one token has
+// parts_per_split partials for each split of its own keys; a longer row of a
+// prefix group one for its own keys (partial nparts - 1 of part_out); the rows of
+// a group also those of the prefix's shards (partials 0 .. shards - 1). A longer
+// row outside every group was written by the packed kernel.
 //
-// One warp per (token, head), the token's row found through tok_row; without
-// prefixes only rows of one token have partials, and a warp takes a (row, head).
-// Lane l holds D / 32 dims. The partials are taken in
-// batches of kMergeBatch whose loads (lse and values together) are all in flight at
-// once; a running maximum joins the batches.
-constexpr int kMergeBatch = 8;
+// Bound by the partials' bytes once many warps are in flight: a warp per (token,
+// head), lane l with D / 32 dims; all it has to know of the token is one 16-byte
+// record, and the loads of a batch of kMergeBatch partials (lse and values
+// together) are all in flight at once; a running maximum joins the batches.
+constexpr int kMergeBatch = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
-    range_merge_kernel(PrefillArgs a, const int32_t* __restrict__ row_grp, const int32_t* __restrict__ grp_shards,
-                       const int32_t* __restrict__ tok_row, const float* __restrict__ dec_out, const float* __restrict__ dec_lse, int max_splits,
-                       int parts_per_split) {
+    range_merge_kernel(PrefillArgs a, const MergeTask* __restrict__ tasks, const float* __restrict__ dec_out,
+                       const float* __restrict__ dec_lse, int max_splits, int parts_per_split) {
     constexpr int kV = D / 32;
     using Vec = typename std::conditional<kV == 4, float4, float2>::type;
     grid_wait();
     const int lane = threadIdx.x % 32;
-    const int64_t task = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    const int32_t at = (int32_t)(task / a.hq), h = (int32_t)(task - (int64_t)at * a.hq);
-    const bool by_token = a.num_prefixes > 0;
-    if (at >= (by_token ? a.total_q : a.num_rows)) return;
-    const int32_t ri = by_token ? tok_row[at] : at;
-    if (ri < 0 || !a.row_ok[ri]) return;
-    const pcp_row_t row = a.rows[ri];
-    const int32_t grp = row_grp[ri];
-    if (row.q_len > 1 && grp < 0) return;
-    const int shards = grp >= 0 ? grp_shards[grp] : 0;
-    const bool one = row.q_len == 1;
+    const int64_t job = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    const int32_t at = (int32_t)(job / a.hq), h = (int32_t)(job - (int64_t)at * a.hq);
+    if (at >= (a.num_prefixes > 0 ? a.total_q : a.num_rows)) return;
+    const int4 raw = *reinterpret_cast<const int4*>(tasks + at);
+    const MergeTask task{raw.x, raw.y, raw.z, raw.w};
+    if (task.row < 0) return;
+    const bool one = task.splits > 0;
+    const int32_t t = one ? task.token : at;
     // partials 0 .. n - 1 are the row's own keys', the others the prefix's shards
-    const int n = one ? parts_per_split * ((key_range(a, row, a.row_lo[ri]).len + a.chunk - 1) / a.chunk) : 1;
-    const size_t base = ((size_t)ri * a.hq + h) * (2 * max_splits);
+    const int n = one ? parts_per_split * task.splits : 1, all = n + task.shards;
+    const size_t base = ((size_t)task.row * a.hq + h) * (2 * max_splits);
     const size_t out_stride = (size_t)a.total_q * a.hq * D, lse_stride = (size_t)a.hq * a.total_q;
-    const int32_t t = by_token ? at : row.q_start;
     const size_t li = (size_t)h * a.total_q + t, o = ((size_t)t * a.hq + h) * D;
     float M = -INFINITY, W = 0.f, O[kV] = {};
-    for (int s0 = 0; s0 < n + shards; s0 += kMergeBatch) {
+    for (int s0 = 0; s0 < all; s0 += kMergeBatch) {
         float ls[kMergeBatch];
         Vec x[kMergeBatch];
 #pragma unroll
         for (int k = 0; k < kMergeBatch; ++k) {
             const int s = s0 + k;
             ls[k] = -INFINITY;
-            if (s >= n + shards) continue;
-            if (one && s < n) {
-                ls[k] = __ldcg(dec_lse + base + s);
-                x[k] = __ldcg(reinterpret_cast<const Vec*>(dec_out + (base + s) * D) + lane);
-            } else {
-                const size_t p = s < n ? a.nparts - 1 : s - n;
-                ls[k] = __ldcg(a.part_lse + p * lse_stride + li);
-                x[k] = __ldcg(reinterpret_cast<const Vec*>(a.part_out + p * out_stride + o) + lane);
-            }
+            if (s >= all) continue;
+            const size_t p = s < n ? a.nparts - 1 : s - n;
+            const bool dec = one && s < n;
+            ls[k] = __ldcg(dec ? dec_lse + base + s : a.part_lse + p * lse_stride + li);
+            x[k] = __ldcg(reinterpret_cast<const Vec*>(dec ? dec_out + (base + s) * D : a.part_out + p * out_stride + o) +
+                          lane);
         }
         float m = M;
 #pragma unroll
@@ -524,7 +522,8 @@ __global__ void __launch_bounds__(256)
     const float inv = W > 0.f ? 1.f / W : 0.f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + o) + lane * (kV / 2);
     if constexpr (kV == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
     else
         *dst = pack_bf16x2(O[0] * inv, O[1] * inv);
     if (lane == 0) a.lse[li] = W > 0.f ? M + __logf(W) : -INFINITY;
@@ -590,24 +589,24 @@ int launch_decode_d(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_
 #define PCP_DECODE_TC 1  // 1: the tensor-core decode where it applies (head_dim 128, G <= 8)
 #endif
 
+// the tensor-core kernel writes a partial per softmax warpgroup over an FP8 cache and
+// with more than 8 q heads per kv head
+int decode_parts(const PrefillArgs& a) {
+    return PCP_DECODE_TC && decode_tc_applies(a) && (a.k_descale || a.hq / a.hkv > 8) ? 2 : 1;
+}
+
 bool decode_side_applies(const PrefillArgs& a) { return PCP_DECODE_TC && decode_tc_applies(a); }
 
 namespace {
 
-// The decode partials of every decode row; *pps: partials per split.
+// The decode partials of every decode row (decode_parts per split).
 int launch_decode_parts(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
-                        cudaStream_t stream, int grid, int* parts) {
+                        cudaStream_t stream, int grid) {
     if (a.d != 64 && a.d != 128) return PCP_ERR_UNSUPPORTED;
     int rc = PCP_DECODE_TC ? launch_decode_tc(a, dec_out, dec_lse, max_splits, stream, grid) : PCP_ERR_UNSUPPORTED;
-    // partials per split: the tensor-core kernel writes one per softmax warpgroup
-    // over an FP8 cache and with more than 8 q heads per kv head
-    int pps = (a.k_descale || a.hq / a.hkv > 8) ? 2 : 1;
-    if (rc == PCP_ERR_UNSUPPORTED) {
+    if (rc == PCP_ERR_UNSUPPORTED)
         rc = a.d == 64 ? launch_decode_d<64>(a, dec_out, dec_lse, max_splits, stream)
                        : launch_decode_d<128>(a, dec_out, dec_lse, max_splits, stream);
-        pps = 1;
-    }
-    *parts = pps;
     return rc;
 }
 
@@ -615,27 +614,24 @@ int launch_decode_parts(const PrefillArgs& a, float* dec_out, float* dec_lse, in
 
 int launch_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                   cudaStream_t stream, int grid) {
-    int pps = 1;
-    const int rc = launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, grid, &pps);
+    const int rc = launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, grid);
     if (rc != PCP_OK) return rc;
-    return launch_merge(a, dec_out, dec_lse, max_splits, pps, stream);
+    return launch_merge(a, dec_out, dec_lse, max_splits, decode_parts(a), stream);
 }
 
-int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, int* parts,
+int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                         cudaStream_t stream) {
-    return launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, 0, parts);
+    return launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, 0);
 }
 
-int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32_t* grp_shards, const int32_t* tok_row,
-                       const float* dec_out, const float* dec_lse, int32_t max_splits, int parts,
-                       cudaStream_t stream) {
-    const int64_t tasks = (int64_t)(a.num_prefixes > 0 ? a.total_q : a.num_rows) * a.hq;
-    const dim3 grid((unsigned)((tasks + 7) / 8));
-    const cudaError_t e =
-        a.d == 64 ? launch_chained(range_merge_kernel<64>, grid, dim3(256), 0, stream, a, row_grp, grp_shards, tok_row,
-                                   dec_out, dec_lse, max_splits, parts)
-                  : launch_chained(range_merge_kernel<128>, grid, dim3(256), 0, stream, a, row_grp, grp_shards, tok_row,
-                                   dec_out, dec_lse, max_splits, parts);
+int launch_range_merge(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out, const float* dec_lse,
+                       int32_t max_splits, int parts, cudaStream_t stream) {
+    const int64_t jobs = (int64_t)(a.num_prefixes > 0 ? a.total_q : a.num_rows) * a.hq;
+    const dim3 grid((unsigned)((jobs + 7) / 8));
+    const cudaError_t e = a.d == 64 ? launch_chained(range_merge_kernel<64>, grid, dim3(256), 0, stream, a, tasks, dec_out,
+                                                     dec_lse, max_splits, parts)
+                                    : launch_chained(range_merge_kernel<128>, grid, dim3(256), 0, stream, a, tasks,
+                                                     dec_out, dec_lse, max_splits, parts);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }

@@ -400,13 +400,6 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int G = a.hq / a.hkv;
     const int32_t bs = a.block_size;
-    const int32_t step = (int32_t)gridDim.x;
-    // item of this CTA in round rd: snake order (forward on even rounds, backward
-    // on odd ones) over the list, whose full splits come first and partial ones
-    // longest first
-    auto item_of_round = [&](int32_t rd) -> int32_t {
-        return rd * step + ((rd & 1) ? step - 1 - (int32_t)blockIdx.x : (int32_t)blockIdx.x);
-    };
     const int32_t* tail_rows = a.dec_pre + a.num_rows + 1;
 
     if (threadIdx.x == 0) {
@@ -448,7 +441,16 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         grid_launch_dependents();
     }
     for (int i = threadIdx.x; i <= a.num_rows; i += tc_threads(F8, GP)) pre[i] = a.dec_pre[i];
-    const int32_t total = a.num_units[1];
+    // CTAs that take items: all of them, or (RNG) as many as the scheduler gave the
+    // decode rows beside the packed kernel's
+    const int32_t step = RNG ? a.num_units[2] : (int32_t)gridDim.x;
+    const int32_t total = !RNG || (int32_t)blockIdx.x < step ? a.num_units[1] : 0;
+    // item of this CTA in round rd: snake order (forward on even rounds, backward
+    // on odd ones) over the list, whose full splits come first and partial ones
+    // longest first
+    auto item_of_round = [&](int32_t rd) -> int32_t {
+        return rd * step + ((rd & 1) ? step - 1 - (int32_t)blockIdx.x : (int32_t)blockIdx.x);
+    };
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -825,6 +827,14 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                         const float f0 = fast_exp2(m_run[h] - M), f1 = fast_exp2(m1 - M);
                         const float L = L0 * f0 + L1 * f1;
                         const float O = acc[h] * f0 + xchg[kGS + h * kKeys + t] * f1;
+                        if (RNG && a.direct) {  // every row is one split: the result itself
+                            const size_t o = ((size_t)it.q_start * a.hq + it.hk * G + h) * kD + t;
+                            reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
+                            if (t == 0)
+                                a.lse[(size_t)(it.hk * G + h) * a.total_q + it.q_start] =
+                                    L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+                            continue;
+                        }
                         const size_t slot = ((size_t)it.ri * a.hq + it.hk * G + h) * (2 * max_splits) + it.split;
                         dec_out[slot * kD + t] = L > 0.f ? O / L : 0.f;
                         if (t == 0) dec_lse[slot] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;

@@ -494,12 +494,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __threadfence();
         grid_launch_dependents();
     }
-    const int32_t total_items = (*a.num_units) * slots_per_unit;
+    // CTAs that take items: all of them, or (PACK) those the scheduler left beside the
+    // decode rows'
+    const int32_t ctas = PACK ? __ldcg(a.num_units + 3) : (int32_t)gridDim.x;
+    const int32_t total_items =
+        !PACK || (int32_t)blockIdx.x < ctas ? (PACK ? __ldcg(a.num_units) : *a.num_units) * slots_per_unit : 0;
     // Item of this CTA in round r: the longest-first list is dealt out in snake
     // order (forward on even rounds, backward on odd ones), which balances the
     // per-CTA totals far better than plain round robin, with no atomics.
     auto item_of_round = [&](int32_t r) -> int32_t {
-        return r * (int32_t)gridDim.x + ((r & 1) ? (int32_t)(gridDim.x - 1 - blockIdx.x) : (int32_t)blockIdx.x);
+        return r * ctas + ((r & 1) ? ctas - 1 - (int32_t)blockIdx.x : (int32_t)blockIdx.x);
     };
     auto item_at = [&](int32_t idx) -> Item {
         if constexpr (PACK) return packed_item(a, idx);
@@ -849,17 +853,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_scores();
                 if constexpr (PACK && !F8) {
                     // slot 0's threads zero the V rows of slots that no query of the item sees
-                    // (cache rows before the window, unwritten ones past the end) before its
-                    // P, and with it this tile's first PV, is released; S(j) done means that
-                    // V(j) has landed
-                    if (g == 0 && !full && !packed_slot_live(item_at(idx), a.sinks, key0 + r)) {
-                        uint8_t* vrow = smem + C::kV + (kt % kNV) * C::kTileBytes + r * 128;
+                    // (cache rows before the window, unwritten ones in the last page) before
+                    // its P, and with it this tile's first PV, is released; S(j) done means that
+                    // V(j) has landed. A warp's lanes start at different 16-byte chunks of their
+                    // rows, which keeps them off each other's banks
+                    if (g == 0 && !full) {
+                        const Item z_it = item_at(idx);
+                        const int32_t v = key0 + r;
+                        if (!packed_slot_live(z_it, a.sinks, v) && v < (z_it.k_end + bs - 1) / bs * bs) {
+                            uint8_t* vrow = smem + C::kV + (kt % kNV) * C::kTileBytes + r * 128;
 #pragma unroll
-                        for (int h2 = 0; h2 < C::kHalves; ++h2)
+                            for (int h2 = 0; h2 < C::kHalves; ++h2)
 #pragma unroll
-                            for (int c2 = 0; c2 < 8; ++c2)
-                                *reinterpret_cast<uint4*>(vrow + h2 * C::kHalfBytes + c2 * 16) = make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();
+                                for (int c2 = 0; c2 < 8; ++c2)
+                                    *reinterpret_cast<uint4*>(vrow + h2 * C::kHalfBytes + ((c2 ^ (r & 7)) << 4)) =
+                                        make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                        }
                     }
                 }
                 // Fast path: every row of the warp already has a finite reference max m;
@@ -1364,7 +1374,12 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
 // nparts - 1, a longer row's own keys partial nparts; a row outside every
 // group attends all its keys into the result at once. row_lo: each row's first
 // own key; row_grp: its group or -1; grp_shards: each group's shards (0: bad);
-// tok_row (shared-prefix calls): the row whose partials make up each token, or -1.
+// merge: what makes up each token (shared-prefix calls) or row (window calls).
+//
+// It also deals the SMs: with both decode rows and packed items, header[2] of them
+// take the decode rows (bound by HBM) while the other header[3] take the packed
+// items (bound by the tensor cores), in proportion to the modelled SM time of
+// each; and it picks the shards of the prefixes for the shortest modelled time.
 //
 // One block, bound by latency: units are dealt to the threads by a search over
 // the rows' running counts (a thread per row would write a long row's units one
@@ -1384,11 +1399,13 @@ __device__ __forceinline__ int32_t last_at_most(const int32_t* off, int32_t n, i
 
 __global__ void __launch_bounds__(kSchedThreads, 1)
     range_schedule_kernel(PrefillArgs a, PackedUnit* units, PackedUnit* sorted, int32_t* header, int32_t* row_ok,
-                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* tok_row, int32_t* dec_pre,
-                          int64_t max_units) {
+                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, MergeTask* merge,
+                          int32_t* dec_pre, int64_t max_units) {
     __shared__ int32_t warp_sums[32];
     __shared__ int32_t tail_cnt[kTailBuckets + 1], tail_off[kTailBuckets + 1], tail_fill[kTailBuckets + 1];
     __shared__ int32_t tail_warp[kSchedThreads / 32][kTailBuckets + 1];
+    __shared__ int32_t cost[4];  // decode items and tiles, packed items and tiles (per kv head)
+    __shared__ int32_t max_shards;
     __shared__ int32_t off[kSchedThreads];       // first unit of each row (group) of the round
     __shared__ int32_t classes[kCostClasses];    // units per cost class, then the class's next place
     grid_launch_dependents();  // the decode kernel sets itself up meanwhile
@@ -1416,13 +1433,14 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         if (!ok) report_status(a.status, PCP_ERR_RANGE);
         grp_shards[g] = ok ? min(a.nparts - 1, (p.prefix_len + kBlockN - 1) / kBlockN) : 0;
     }
+    if (threadIdx.x < 4) cost[threadIdx.x] = 0;
     if (ng > 0)
-        for (int32_t t = threadIdx.x; t < a.total_q; t += kSchedThreads) tok_row[t] = -1;
+        for (int32_t t = threadIdx.x; t < a.total_q; t += kSchedThreads) merge[t] = MergeTask{-1, 0, 0, 0};
     __syncthreads();
     int32_t base = 0, dbase = 0;
     for (int32_t r0 = 0; r0 < num_rows; r0 += kSchedThreads) {
         const int32_t ri = r0 + threadIdx.x;
-        int32_t cnt = 0, dcnt = 0;
+        int32_t cnt = 0, dcnt = 0, splits = 0;
         if (ri < num_rows) {
             const pcp_row_t row = a.rows[ri];
             int32_t lo = 0, grp = -1;
@@ -1453,8 +1471,13 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
                 dcnt = (nv / a.chunk) * a.hkv;
                 const int32_t part = nv % a.chunk;
                 if (part) atomicAdd(&tail_cnt[(part + kBlockN - 1) / kBlockN], 1);
-                if (ng > 0) tok_row[row.q_start] = ri;
+                splits = (nv + a.chunk - 1) / a.chunk;
+                atomicAdd(&cost[0], splits);
+                atomicAdd(&cost[1], (nv + kBlockN - 1) / kBlockN);
             }
+            const MergeTask m{splits > 0 ? ri : -1, row.q_start, splits, grp >= 0 ? grp_shards[grp] : 0};
+            if (ng == 0) merge[ri] = m;
+            else if (splits > 0) merge[row.q_start] = m;
         }
         int32_t dtot;
         const int32_t doff = dbase + block_exclusive_scan(dcnt, warp_sums, &dtot);
@@ -1470,6 +1493,8 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
                                              row_lo[r0 + i], row.kv_end, row_grp[r0 + i] >= 0 ? a.nparts : 0);
             units[base + u] = x;
             atomicAdd(&classes[class_of(x)], 1);
+            atomicAdd(&cost[2], 1);
+            atomicAdd(&cost[3], (x.k_end + kBlockN - 1) / kBlockN);
         }
         if (ng > 0)  // a warp per unit
             for (int32_t u = warp; u < tot; u += kSchedThreads / 32) {
@@ -1477,11 +1502,57 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
                 if (row_grp[r0 + i] < 0) continue;
                 const pcp_row_t row = a.rows[r0 + i];
                 const int32_t t1 = min(row.q_len, (u - off[i] + 1) * span);
-                for (int32_t t = (u - off[i]) * span + lane; t < t1; t += 32) tok_row[row.q_start + t] = r0 + i;
+                const MergeTask m{r0 + i, 0, 0, grp_shards[row_grp[r0 + i]]};
+                for (int32_t t = (u - off[i]) * span + lane; t < t1; t += 32) merge[row.q_start + t] = m;
             }
         base += tot;
         __syncthreads();  // off is rewritten
     }
+    // The SMs of the decode rows and the prefixes' shards: lane n - 1 of warp 0 models n
+    // shards. SM times measured on GB300 (us): a decode item 1 and a 128-key tile 0.95
+    // (FP8 1.15) on a few SMs, a packed item 4.5 and a tile 1.75, a partial to merge
+    // total_q x hq x d x 8 bytes at 10 TB/s.
+    __syncthreads();
+    if (warp == 0) {
+        const float dec_us = (float)a.hkv * (1.0f * cost[0] + (a.k_descale ? 1.15f : 0.95f) * cost[1]);
+        const float merge_us = (float)a.total_q * a.hq * a.d * 8e-7f;
+        const int32_t nsm = a.num_sms, most = min(32, max(1, a.nparts - 1));
+        float items = (float)cost[2], tiles = (float)cost[3];
+        int32_t longest = 0;
+        for (int32_t g = 0; g < ng; ++g) {
+            if (grp_shards[g] == 0) continue;
+            const pcp_prefix_t p = a.prefixes[g];
+            const int32_t t = (p.prefix_len + kBlockN - 1) / kBlockN, tok = (p.q_len + span - 1) / span;
+            const int32_t n = min(lane + 1, grp_shards[g]);
+            items += (float)(tok * n);
+            tiles += (float)tok * t;
+            longest = max(longest, (t + n - 1) / n);
+        }
+        const float pack_us = (float)a.hkv * (4.5f * items + 1.75f * tiles);
+        int32_t k = 0;
+        if (a.overlap && dec_us > 0.f && pack_us > 0.f)
+            k = max(1, min(nsm - 1, (int32_t)(nsm * dec_us / (dec_us + pack_us) + 0.5f)));
+        const float m = (float)(nsm - k);
+        const float rounds = ceilf(items * a.hkv / m);
+        float us = fmaxf(items > 0.f ? rounds * pack_us / (a.hkv * items) : 0.f, 4.5f + 1.75f * longest);
+        if (k > 0) us = fmaxf(us, dec_us / k);
+        us += (lane + 1) * merge_us;
+        if (lane >= most) us = INFINITY;
+        float best = us;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        const int pick = __ffs(__ballot_sync(0xffffffffu, us == best)) - 1;
+        if (lane == pick) {
+            max_shards = lane + 1;
+            header[2] = k > 0 ? k : nsm;
+            header[3] = nsm - k;
+        }
+    }
+    __syncthreads();
+    for (int32_t g = threadIdx.x; g < ng; g += kSchedThreads) grp_shards[g] = min(grp_shards[g], max_shards);
+    for (int32_t t = threadIdx.x; t < a.total_q && ng > 0; t += kSchedThreads)
+        merge[t].shards = min(merge[t].shards, max_shards);
+    __syncthreads();
     for (int32_t g0 = 0; g0 < ng; g0 += kSchedThreads) {
         const int32_t g = g0 + threadIdx.x;
         int32_t cnt = 0;
@@ -1644,10 +1715,10 @@ int launch_schedule(const PrefillArgs& a, int32_t flags, Unit* units, Unit* unit
 }
 
 int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header,
-                          int32_t* row_ok, int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* tok_row,
+                          int32_t* row_ok, int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, MergeTask* merge,
                           int32_t* dec_pre, int64_t max_units, cudaStream_t stream) {
     range_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(a, units, units_sorted, header, row_ok, row_lo, row_grp,
-                                                           grp_shards, tok_row, dec_pre, max_units);
+                                                           grp_shards, merge, dec_pre, max_units);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;

@@ -39,6 +39,15 @@ struct alignas(16) PackedUnit {
     int32_t shift, k_end;  // slots of the walk: key = slot + shift past the sinks; its length
 };
 
+// What makes up the result of a token (shared-prefix calls; indexed by token) or
+// of a one-token row (window calls; by row): row is -1 where the merge has
+// nothing to do.
+struct alignas(16) MergeTask {
+    int32_t row, token;  // token: of a one-token row (a longer row's tokens are their index)
+    int32_t splits;      // decode splits of a one-token row; 0: a longer row, its own keys in one partial
+    int32_t shards;      // of its group's prefix
+};
+
 // Workspace layout of pcp_attn_varlen (all offsets 256-byte aligned).
 struct WorkspaceLayout {
     size_t header;        // int32[64]: [0] = number of units
@@ -114,6 +123,9 @@ struct PrefillArgs {
     // chunk is 0 in the others, which read none of these.
     int32_t chunk;              // keys per decode split, a multiple of 128, at most kDecodeChunk
     int32_t window, sinks;      // keys a query sees: the last `window` ones and the first `sinks`
+    int32_t num_sms;            // CTAs of the persistent kernels
+    int32_t overlap;            // the decode kernel is the persistent one: it can share the SMs
+    int32_t direct;             // decode rows have one partial each: written straight to out and lse
     int32_t slots;              // token tiles per packed item: 1 or 2
     const PackedUnit* packed;   // the packed work list, longest first
     const int32_t* row_lo;      // first own key of each row (0, or its group's prefix length)
@@ -209,18 +221,20 @@ int launch_decode_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32
 // True when launch_decode takes the tensor-core kernel for these arguments (the
 // persistent kernel that PCP_ATTN_DECODE_SMS confines to a few SMs).
 bool decode_side_applies(const PrefillArgs& a);
+// Partials per split of the decode rows: two where the tensor-core kernel writes one
+// per softmax warpgroup.
+int decode_parts(const PrefillArgs& a);
 int launch_separate_merge(const PrefillArgs& a, cudaStream_t stream);
 // Window and shared-prefix calls: the schedule, the packed kernel over its work
-// list, the decode partials (*parts: partials per split) and their merge.
+// list, the decode partials (decode_parts per split) and their merge.
 int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header,
-                          int32_t* row_ok, int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, int32_t* tok_row,
+                          int32_t* row_ok, int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, MergeTask* merge,
                           int32_t* dec_pre, int64_t max_units, cudaStream_t stream);
 int launch_packed(const PrefillArgs& a, cudaStream_t stream);
-int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, int* parts,
+int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                         cudaStream_t stream);
-int launch_range_merge(const PrefillArgs& a, const int32_t* row_grp, const int32_t* grp_shards, const int32_t* tok_row,
-                       const float* dec_out, const float* dec_lse, int32_t max_splits, int parts,
-                       cudaStream_t stream);
+int launch_range_merge(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out, const float* dec_lse,
+                       int32_t max_splits, int parts, cudaStream_t stream);
 int launch_cache_write(const void* k, const void* v, const int64_t* slot, int32_t num_tokens,
                        int32_t vec_per_tok, void* key_cache, void* value_cache, int64_t num_slots,
                        int32_t* status, cudaStream_t stream);

@@ -19,7 +19,7 @@ constexpr int kMaxPrefixes = 1024;
 constexpr int kMaxShards = 32;     // shards of a prefix
 
 struct RangeLayout {
-    size_t header, row_ok, row_lo, row_grp, grp_shards, tok_row, dec_pre, units, units_sorted, part_out, part_lse, dec_out,
+    size_t header, row_ok, row_lo, row_grp, grp_shards, merge, dec_pre, units, units_sorted, part_out, part_lse, dec_out,
         dec_lse, total;
     int64_t max_units;
     int32_t slots, chunk, max_splits, nparts;
@@ -45,25 +45,15 @@ int32_t decode_chunk(int32_t num_rows, int32_t hkv, int64_t max_len) {
     return best_chunk;
 }
 
-// Shards of each prefix: the count with the shortest modelled time. An SM takes
-// its share of the items one after the other; an item costs about 2.3 key tiles
-// of start and end on top of the tiles it walks (measured on the prefill
-// kernel), and every shard one more fp32 partial to merge.
-int32_t prefix_shards(int32_t total_q, int32_t hq, int32_t hkv, int32_t d, int32_t span, int64_t max_kv) {
+// The most shards of a prefix (its partials take workspace; the scheduler picks how
+// many): enough to give every SM four items.
+int32_t most_shards(int32_t total_q, int32_t hkv, int32_t span, int64_t max_kv) {
     const int64_t items = (total_q + span - 1) / span * (int64_t)hkv;
     const int64_t tiles = (max_kv + kBlockN - 1) / kBlockN;
-    const double merge = (double)total_q * hq * d * 8 / 1e13 * 1e6 / 1.8;  // in tiles of 1.8 us, at L2 speed
-    double best = 0;
-    int32_t n_best = 1;
-    for (int32_t n = 1; n <= kMaxShards && n <= (tiles > 1 ? tiles / 2 : 1); ++n) {
-        const double rounds = (double)((items * n + kSms - 1) / kSms);
-        const double t = rounds * (2.3 + (double)((tiles + n - 1) / n)) + n * merge;
-        if (n == 1 || t < best) {
-            best = t;
-            n_best = n;
-        }
-    }
-    return n_best;
+    int64_t n = items > 0 ? (4 * kSms + items - 1) / items + 1 : 1;
+    if (n > tiles / 2) n = tiles / 2;
+    if (n > kMaxShards) n = kMaxShards;
+    return n > 1 ? (int32_t)n : 1;
 }
 
 // num_prefixes < 0: a window call.
@@ -76,7 +66,7 @@ RangeLayout range_layout(int32_t num_rows, int32_t num_prefixes, int32_t total_q
     w.chunk = decode_chunk(num_rows, hkv, max_len);
     w.max_splits = max_len > 0 ? (int32_t)((max_len + w.chunk - 1) / w.chunk) : 1;
     const int32_t ng = num_prefixes > 0 ? num_prefixes : 0;
-    const int32_t shards = ng > 0 ? prefix_shards(total_q, hq, hkv, d, span, max_kv) : 0;
+    const int32_t shards = ng > 0 ? most_shards(total_q, hkv, span, max_kv) : 0;
     w.nparts = ng > 0 ? shards + 1 : 0;
     const int64_t tiles = (total_q + span - 1) / span;
     w.max_units = tiles + num_rows + shards * (tiles + ng);
@@ -91,7 +81,7 @@ RangeLayout range_layout(int32_t num_rows, int32_t num_prefixes, int32_t total_q
     w.row_lo = take((size_t)num_rows * 4);
     w.row_grp = take((size_t)num_rows * 4);
     w.grp_shards = take((size_t)ng * 4);
-    w.tok_row = take(ng > 0 ? (size_t)total_q * 4 : 0);
+    w.merge = take((size_t)(ng > 0 ? total_q : num_rows) * sizeof(MergeTask));
     w.dec_pre = take((2 * (size_t)num_rows + 1) * 4);
     w.units = take((size_t)w.max_units * sizeof(PackedUnit));
     w.units_sorted = take((size_t)w.max_units * sizeof(PackedUnit));
@@ -205,15 +195,19 @@ int range_call(const RangeCall& c) {
     a.prefixes = c.prefixes;
     a.num_prefixes = shared ? c.num_prefixes : 0;
 
+    const int parts = decode_parts(a);
+    a.num_sms = num_sms();
+    a.overlap = decode_side_applies(a);
+    a.direct = !shared && w.max_splits == 1 && parts == 1;
+    MergeTask* tasks = reinterpret_cast<MergeTask*>(ws + w.merge);
     int rc = launch_range_schedule(a, reinterpret_cast<PackedUnit*>(ws + w.units),
-                                   reinterpret_cast<PackedUnit*>(ws + w.units_sorted),
-                                   ints(w.header), ints(w.row_ok), ints(w.row_lo), ints(w.row_grp),
-                                   ints(w.grp_shards), ints(w.tok_row), ints(w.dec_pre), w.max_units, c.stream);
+                                   reinterpret_cast<PackedUnit*>(ws + w.units_sorted), ints(w.header), ints(w.row_ok),
+                                   ints(w.row_lo), ints(w.row_grp), ints(w.grp_shards), tasks, ints(w.dec_pre),
+                                   w.max_units, c.stream);
     if (rc != PCP_OK) return rc;
     float* dec_out = reinterpret_cast<float*>(ws + w.dec_out);
     float* dec_lse = reinterpret_cast<float*>(ws + w.dec_lse);
-    int parts = 1;
-    rc = launch_range_decode(a, dec_out, dec_lse, w.max_splits, &parts, c.stream);
+    rc = launch_range_decode(a, dec_out, dec_lse, w.max_splits, c.stream);
     if (rc != PCP_OK) return rc;
     // no row can have two tokens when there are as many rows as tokens (the rows'
     // tokens are disjoint): only prefixes are left for the packed kernel
@@ -221,8 +215,8 @@ int range_call(const RangeCall& c) {
         rc = launch_packed(a, c.stream);
         if (rc != PCP_OK) return rc;
     }
-    return launch_range_merge(a, ints(w.row_grp), ints(w.grp_shards), ints(w.tok_row), dec_out, dec_lse, w.max_splits,
-                              parts, c.stream);
+    if (a.direct) return PCP_OK;
+    return launch_range_merge(a, tasks, dec_out, dec_lse, w.max_splits, parts, c.stream);
 }
 
 bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
