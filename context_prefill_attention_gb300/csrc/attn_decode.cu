@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(256)
     const int32_t at = (int32_t)(job / a.hq), h = (int32_t)(job - (int64_t)at * a.hq);
     if (at >= (a.num_prefixes > 0 ? a.total_q : a.num_rows)) return;
     const int4 raw = *reinterpret_cast<const int4*>(tasks + at);
-    const MergeTask task{raw.x, raw.y, raw.z, raw.w};
+    const MergeTask task{raw.x, raw.y, raw.z, min(raw.w, a.num_units[4])};
     if (task.row < 0) return;
     const bool one = task.splits > 0;
     const int32_t t = one ? task.token : at;

@@ -140,7 +140,9 @@ static_assert(TcCfg<true, 4>::kQC % 1024 == 0 && TcCfg<true, 8>::kP % 1024 == 0 
 
 struct DecItem {
     int32_t ri, req, q_start, hk, split, lo, hi, nt;
-    KeyRange kr;  // RNG: lo and hi count slots of this walk
+    int32_t sinks, gap_end, shift;  // RNG (DecUnit): lo and hi count slots of the row's walk
+    // RNG: whether slot v holds a key that the row sees
+    __device__ __forceinline__ bool live(int32_t v) const { return v < sinks || v >= gap_end; }
 };
 
 // Item p of the decode work list: first every full kDecodeChunk-key split (row
@@ -149,35 +151,49 @@ struct DecItem {
 // in the order of tail_rows (longest partial first). Dealt in snake order, the
 // CTAs then end within a fraction of a split of each other. The caller's items
 // rise, so the row cursor ri only walks forward over the prefix.
-// RNG (window and shared-prefix calls): the row's own keys (key_range) in splits
-// of a.chunk.
+// RNG (window and shared-prefix calls): the scheduler's list holds the splits
+// themselves, longest first.
 template <bool RNG>
 __device__ __forceinline__ DecItem dec_item(const int32_t* pre, int32_t& ri, int32_t p, const PrefillArgs& a,
                                             const int32_t* tail_rows) {
-    const int32_t num_rows = a.num_rows, hkv = a.hkv, chunk = RNG ? a.chunk : kDecodeChunk;
-    const int32_t nfull = pre[num_rows];
-    const bool full = p < nfull;
-    int32_t r, rem;
-    if (full) {
-        while (pre[ri + 1] <= p) ++ri;
-        r = ri;
-        rem = p - pre[r];
+    const int32_t num_rows = a.num_rows, hkv = a.hkv;
+    DecItem it{};
+    if constexpr (RNG) {
+        const int32_t n = p / hkv;
+        const int4* src = reinterpret_cast<const int4*>(a.dec_units + n);
+        const int4 x = src[0], y = src[1];
+        it.ri = x.x;
+        it.req = x.y;
+        it.q_start = x.z;
+        it.hk = p - n * hkv;
+        it.lo = x.w;
+        it.hi = y.x;
+        it.split = it.lo / a.chunk;
+        it.sinks = y.y;
+        it.gap_end = y.z;
+        it.shift = y.w;
     } else {
-        rem = p - nfull;
-        r = tail_rows[rem / hkv];
+        const int32_t nfull = pre[num_rows];
+        const bool full = p < nfull;
+        int32_t r, rem;
+        if (full) {
+            while (pre[ri + 1] <= p) ++ri;
+            r = ri;
+            rem = p - pre[r];
+        } else {
+            rem = p - nfull;
+            r = tail_rows[rem / hkv];
+        }
+        const pcp_row_t row = a.rows[r];
+        const int32_t nf = row.kv_end / kDecodeChunk;  // full splits of the row (>= 1 on the full side)
+        it.ri = r;
+        it.req = row.req;
+        it.q_start = row.q_start;
+        it.hk = full ? rem / nf : rem % hkv;
+        it.split = full ? rem % nf : nf;
+        it.lo = it.split * kDecodeChunk;
+        it.hi = min(row.kv_end, it.lo + kDecodeChunk);
     }
-    const pcp_row_t row = a.rows[r];
-    DecItem it;
-    if constexpr (RNG) it.kr = key_range(a, row, a.row_lo[r]);
-    const int32_t len = RNG ? it.kr.len : row.kv_end;
-    const int32_t nf = len / chunk;  // full splits of the row (>= 1 on the full side)
-    it.ri = r;
-    it.req = row.req;
-    it.q_start = row.q_start;
-    it.hk = full ? rem / nf : rem % hkv;
-    it.split = full ? rem % nf : nf;
-    it.lo = it.split * chunk;
-    it.hi = min(len, it.lo + chunk);
     it.nt = (it.hi - it.lo + kKeys - 1) / kKeys;
     return it;
 }
@@ -440,7 +456,8 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         grid_wait();
         grid_launch_dependents();
     }
-    for (int i = threadIdx.x; i <= a.num_rows; i += tc_threads(F8, GP)) pre[i] = a.dec_pre[i];
+    if constexpr (!RNG)
+        for (int i = threadIdx.x; i <= a.num_rows; i += tc_threads(F8, GP)) pre[i] = a.dec_pre[i];
     // CTAs that take items: all of them, or (RNG) as many as the scheduler gave the
     // decode rows beside the packed kernel's
     const int32_t step = RNG ? a.num_units[2] : (int32_t)gridDim.x;
@@ -484,7 +501,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
             __syncwarp();
             for (int i = lane; i < npg; i += 32) {
                 int32_t pg = pg0 + i;
-                if (RNG && pg * bs >= it.kr.sink_slots) pg += it.kr.shift / bs;
+                if (RNG && pg * bs >= it.sinks) pg += it.shift / bs;  // (a page begun by sinks holds them)
                 const int32_t id = pg < a.max_blocks ? __ldg(table + pg) : -1;
                 int32_t y = oob;
                 if (id >= 0 && id < a.num_blocks) y = id * bs;
@@ -647,7 +664,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 const int nvalid = min(kKeys, it.hi - it.lo - j * kKeys);
                 if (!(ok = mbar_wait_warp(vc_full(vs), (g / kVS) & 1, abort_flag))) break;
                 widen_tile(smem + C::kV + vs * C::kTileBytes, nvalid, ct,
-                           [&](int r) { return !RNG || it.kr.live(it.lo + j * kKeys + r); });
+                           [&](int r) { return !RNG || it.live(it.lo + j * kKeys + r); });
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_full(vs));
@@ -717,7 +734,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 const uint32_t g = gt + j;
                 if ((int)(g & 1) != wg) continue;
                 const int nvalid = min(kKeys, it.hi - it.lo - j * kKeys);
-                const bool valid = t < nvalid && (!RNG || it.kr.live(it.lo + j * kKeys + t));
+                const bool valid = t < nvalid && (!RNG || it.live(it.lo + j * kKeys + t));
                 ok &= mbar_wait_warp(s_full(g & 1), (g >> 1) & 1, abort_flag);
                 tc_fence_after();
                 uint32_t s[kNS];
@@ -758,7 +775,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                     *reinterpret_cast<uint16_t*>(pcol + (kGS + h) * 128 + ((chunk ^ (h & 7)) << 4)) = lo;
                 }
                 // RNG: also where the tile holds slots between the sinks and the window
-                const bool gaps = RNG && it.lo + j * kKeys < it.kr.lo - it.kr.shift && it.kr.lo - it.kr.shift > it.kr.sinks;
+                const bool gaps = RNG && it.lo + j * kKeys < it.gap_end && it.gap_end > it.sinks;
                 if (!F8 && (nvalid < kKeys || gaps)) {
                     // keys past the split's end: zero their V rows (unwritten cache slots in
                     // the last page, stale rows after it) once the tile has landed

@@ -1364,96 +1364,106 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
     for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) sorted[i] = units[(int32_t)(keys[i] & 0xFFFFFFFFu)];
 }
 
-// The scheduler of the window and shared-prefix calls: the row checks, the
-// packed work list (packed_unit; longest first) and the decode work items, as
-// schedule_kernel lays them out but over each row's own keys and in splits of
-// a.chunk keys. A row of one token is a decode row whatever its flag. Window
-// calls (no prefixes): one unit per a.slots tiles of a longer row. Shared-prefix
-// calls: a group's units, per a.slots tiles of its tokens and shard of its
-// prefix (a.nparts - 1 shards of whole pages at most), write partials 1 ..
-// nparts - 1, a longer row's own keys partial nparts; a row outside every
-// group attends all its keys into the result at once. row_lo: each row's first
-// own key; row_grp: its group or -1; grp_shards: each group's shards (0: bad);
-// merge: what makes up each token (shared-prefix calls) or row (window calls).
+// The scheduler of the window and shared-prefix calls: the row checks and the work
+// lists, over each row's own keys. A row of one token is a decode row whatever its flag.
+//  * packed list (packed_unit), longest first. Window calls: one unit per a.slots
+//    tiles of a longer row. Shared-prefix calls: a group's units, per a.slots
+//    tiles of its tokens and shard of its prefix (whole pages), write partials 1 ..
+//    shards; a longer row's own keys partial nparts; a row outside every group
+//    attends all its keys into the result at once.
+//  * decode list (DecUnit): the splits of the decode rows, longest first and in row
+//    order among equals, so that every sum's order is the same in every run (up to
+//    kDecTcMaxRows rows, which is what the kernel that takes it does).
+//  * merge: what makes up each token (shared-prefix calls) or row (window calls).
+//  * header: packed units, decode items, the SMs of each, the most shards of a
+//    prefix. With both decode rows and packed items, some SMs take the decode rows
+//    (bound by HBM) while the others take the packed items (bound by the tensor
+//    cores), in proportion to the modelled SM time of each; the shards of the
+//    prefixes are picked for the shortest modelled time.
 //
-// It also deals the SMs: with both decode rows and packed items, header[2] of them
-// take the decode rows (bound by HBM) while the other header[3] take the packed
-// items (bound by the tensor cores), in proportion to the modelled SM time of
-// each; and it picks the shards of the prefixes for the shortest modelled time.
-//
-// One block, bound by latency: units are dealt to the threads by a search over
-// the rows' running counts (a thread per row would write a long row's units one
-// by one), and ordered by one counting pass over kCostClasses cost classes.
+// One block, bound by latency, so a thread keeps what it has read: prefixes and row
+// fields in shared memory, its first unit in registers; units are dealt to the
+// threads by a search over the rows' running counts (a thread per row would
+// write a long row's units one by one) and ordered by one counting pass.
+constexpr int kMaxGroups = kSchedThreads;
 constexpr int kCostClasses = kSchedThreads;
 
-// Index of the last entry of off[0, n) that is at most u (off ascending, off[0] <= u).
-__device__ __forceinline__ int32_t last_at_most(const int32_t* off, int32_t n, int32_t u) {
-    int32_t lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) / 2;
-        if (off[mid] <= u) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+// Index of the last entry of off[0, kSchedThreads) that is at most u (off ascending from 0).
+__device__ __forceinline__ int32_t last_at_most(const int32_t* off, int32_t u) {
+    int32_t at = 0;
+#pragma unroll
+    for (int step = kSchedThreads / 2; step > 0; step /= 2)
+        if (off[at + step] <= u) at += step;
+    return at;
 }
 
 __global__ void __launch_bounds__(kSchedThreads, 1)
     range_schedule_kernel(PrefillArgs a, PackedUnit* units, PackedUnit* sorted, int32_t* header, int32_t* row_ok,
-                          int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, MergeTask* merge,
-                          int32_t* dec_pre, int64_t max_units) {
+                          int32_t* row_lo, MergeTask* merge, DecUnit* dec_units, int64_t max_units) {
     __shared__ int32_t warp_sums[32];
     __shared__ int32_t tail_cnt[kTailBuckets + 1], tail_off[kTailBuckets + 1], tail_fill[kTailBuckets + 1];
     __shared__ int32_t tail_warp[kSchedThreads / 32][kTailBuckets + 1];
-    __shared__ int32_t cost[4];  // decode items and tiles, packed items and tiles (per kv head)
-    __shared__ int32_t max_shards;
+    __shared__ __align__(16) pcp_prefix_t prefix[kMaxGroups];
+    __shared__ int32_t shards_of[kMaxGroups];    // 0: a bad group
     __shared__ int32_t off[kSchedThreads];       // first unit of each row (group) of the round
+    __shared__ int32_t lo_of[kSchedThreads], grp_of[kSchedThreads];
     __shared__ int32_t classes[kCostClasses];    // units per cost class, then the class's next place
+    __shared__ int32_t cost[4];  // decode splits and tiles, packed units and tiles (per kv head)
+    __shared__ int32_t max_shards;
     grid_launch_dependents();  // the decode kernel sets itself up meanwhile
-    if (threadIdx.x <= kTailBuckets) {
-        tail_cnt[threadIdx.x] = 0;
-        tail_fill[threadIdx.x] = 0;
-    }
-    classes[threadIdx.x] = 0;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int32_t num_rows = a.num_rows, bs = a.block_size, ng = a.num_prefixes;
     const int32_t span = a.slots * (kBlockM / (a.hq / a.hkv));
     const int64_t max_kv = (int64_t)a.max_blocks * bs;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    // the first round's row is on its way while the groups are checked
+    pcp_row_t row{};
+    if (tid < num_rows) row = a.rows[tid];
+    if (tid <= kTailBuckets) {
+        tail_cnt[tid] = 0;
+        tail_fill[tid] = 0;
+    }
+    if (tid < 4) cost[tid] = 0;
+    classes[tid] = 0;
+    if (tid < ng) prefix[tid] = a.prefixes[tid];
+    if (ng > 0)
+        for (int32_t t = tid; t < a.total_q; t += kSchedThreads) merge[t] = MergeTask{-1, 0, 0, 0};
+    __syncthreads();
+    // groups: fields in range, and the tokens after those of every earlier group
+    if (tid < ng) {
+        const pcp_prefix_t p = prefix[tid];
+        bool ok = p.q_start >= 0 && p.q_len >= 1 && (int64_t)p.q_start + p.q_len <= a.total_q && p.req >= 0 &&
+                  p.req < a.num_reqs && p.prefix_len >= 1 && p.prefix_len <= max_kv;
+        for (int32_t e = 0; e < tid && ok; ++e) ok = (int64_t)p.q_start >= (int64_t)prefix[e].q_start + prefix[e].q_len;
+        if (!ok) report_status(a.status, PCP_ERR_RANGE);
+        shards_of[tid] = ok ? min(a.nparts - 1, (p.prefix_len + kBlockN - 1) / kBlockN) : 0;
+    }
+    if (ng > 0) __syncthreads();
     auto class_of = [](const PackedUnit& u) {
         return kCostClasses - 1 - min((u.k_end + kBlockN - 1) / kBlockN, kCostClasses - 1);
     };
-    // groups: fields in range, and the tokens after those of every earlier group
-    for (int32_t g = threadIdx.x; g < ng; g += kSchedThreads) {
-        const pcp_prefix_t p = a.prefixes[g];
-        bool ok = p.q_start >= 0 && p.q_len >= 1 && (int64_t)p.q_start + p.q_len <= a.total_q && p.req >= 0 &&
-                  p.req < a.num_reqs && p.prefix_len >= 1 && p.prefix_len <= max_kv;
-        for (int32_t e = 0; e < g && ok; ++e) {
-            const pcp_prefix_t o = a.prefixes[e];
-            ok = (int64_t)p.q_start >= (int64_t)o.q_start + o.q_len;
-        }
-        if (!ok) report_status(a.status, PCP_ERR_RANGE);
-        grp_shards[g] = ok ? min(a.nparts - 1, (p.prefix_len + kBlockN - 1) / kBlockN) : 0;
-    }
-    if (threadIdx.x < 4) cost[threadIdx.x] = 0;
-    if (ng > 0)
-        for (int32_t t = threadIdx.x; t < a.total_q; t += kSchedThreads) merge[t] = MergeTask{-1, 0, 0, 0};
-    __syncthreads();
-    int32_t base = 0, dbase = 0;
+    PackedUnit mine{};  // unit tid, if there is one
+    // unit i of the list, by the thread of i's place in its round of kSchedThreads
+    auto put = [&](int32_t i, const PackedUnit& x) {
+        if (i < kSchedThreads) mine = x;
+        else units[i] = x;
+        atomicAdd(&classes[class_of(x)], 1);
+    };
+    int32_t base = 0;          // packed units so far
+    int32_t my_lo = 0, my_len = 0, my_splits = 0;  // the first round's row, as a decode row (0 splits: none)
     for (int32_t r0 = 0; r0 < num_rows; r0 += kSchedThreads) {
-        const int32_t ri = r0 + threadIdx.x;
-        int32_t cnt = 0, dcnt = 0, splits = 0;
+        const int32_t ri = r0 + tid;
+        if (r0 > 0 && ri < num_rows) row = a.rows[ri];
+        int32_t cnt = 0, splits = 0, dec_tiles = 0, lo = 0, grp = -1;
         if (ri < num_rows) {
-            const pcp_row_t row = a.rows[ri];
-            int32_t lo = 0, grp = -1;
             // (without prefixes the packed kernel is not launched for num_rows >= total_q)
             bool ok = row_in_range(row, a.num_reqs, a.total_q, max_kv) &&
                       (row.q_len == 1 || ng > 0 || a.total_q > num_rows);
             for (int32_t g = 0; g < ng && ok; ++g) {
-                const pcp_prefix_t p = a.prefixes[g];
+                const pcp_prefix_t p = prefix[g];
                 const int64_t p1 = (int64_t)p.q_start + p.q_len, r1 = (int64_t)row.q_start + row.q_len;
                 if (r1 <= p.q_start || row.q_start >= p1) continue;
                 // the row's tokens lie inside the group, past the prefix
-                ok = grp_shards[g] > 0 && row.q_start >= p.q_start && r1 <= p1 &&
-                     row.kv_end - row.q_len >= p.prefix_len;
+                ok = shards_of[g] > 0 && row.q_start >= p.q_start && r1 <= p1 && row.kv_end - row.q_len >= p.prefix_len;
                 grp = g;
                 lo = p.prefix_len;
             }
@@ -1464,49 +1474,57 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
             }
             row_ok[ri] = ok ? 1 : 0;
             row_lo[ri] = lo;
-            row_grp[ri] = grp;
             if (ok && row.q_len > 1) cnt = (row.q_len + span - 1) / span;
             if (ok && row.q_len == 1) {
-                const int32_t nv = key_range(a, row, lo).len;
-                dcnt = (nv / a.chunk) * a.hkv;
-                const int32_t part = nv % a.chunk;
+                const int32_t len = key_range(a, row, lo).len, part = len % a.chunk;
+                splits = (len + a.chunk - 1) / a.chunk;
+                if (len >= a.chunk) atomicAdd(&tail_cnt[a.chunk / kBlockN], len / a.chunk);
                 if (part) atomicAdd(&tail_cnt[(part + kBlockN - 1) / kBlockN], 1);
-                splits = (nv + a.chunk - 1) / a.chunk;
-                atomicAdd(&cost[0], splits);
-                atomicAdd(&cost[1], (nv + kBlockN - 1) / kBlockN);
+                dec_tiles = (len + kBlockN - 1) / kBlockN;
+                if (r0 == 0) {
+                    my_lo = lo;
+                    my_len = len;
+                    my_splits = splits;
+                }
             }
-            const MergeTask m{splits > 0 ? ri : -1, row.q_start, splits, grp >= 0 ? grp_shards[grp] : 0};
+            const MergeTask m{splits > 0 ? ri : -1, row.q_start, splits, grp >= 0 ? shards_of[grp] : 0};
             if (ng == 0) merge[ri] = m;
             else if (splits > 0) merge[row.q_start] = m;
         }
-        int32_t dtot;
-        const int32_t doff = dbase + block_exclusive_scan(dcnt, warp_sums, &dtot);
-        if (ri < num_rows) dec_pre[ri] = doff;
-        dbase += dtot;
-        int32_t tot;
-        off[threadIdx.x] = block_exclusive_scan(cnt, warp_sums, &tot);
-        __syncthreads();
-        for (int32_t u = threadIdx.x; u < tot && base + u < max_units; u += kSchedThreads) {
-            const int32_t i = last_at_most(off, kSchedThreads, u);
-            const pcp_row_t row = a.rows[r0 + i];
-            const PackedUnit x = packed_unit(a, row.req, row.q_start, row.q_len, row.kv_end - row.q_len, u - off[i], span,
-                                             row_lo[r0 + i], row.kv_end, row_grp[r0 + i] >= 0 ? a.nparts : 0);
-            units[base + u] = x;
-            atomicAdd(&classes[class_of(x)], 1);
-            atomicAdd(&cost[2], 1);
-            atomicAdd(&cost[3], (x.k_end + kBlockN - 1) / kBlockN);
+        const int32_t warp_splits = __reduce_add_sync(0xffffffffu, splits);
+        const int32_t warp_tiles = __reduce_add_sync(0xffffffffu, dec_tiles);
+        if (lane == 0 && warp_splits > 0) {
+            atomicAdd(&cost[0], warp_splits);
+            atomicAdd(&cost[1], warp_tiles);
         }
+        lo_of[tid] = lo;
+        grp_of[tid] = grp;
+        if (a.total_q <= num_rows && ng == 0) continue;  // no row is longer than one token
+        int32_t tot;
+        off[tid] = block_exclusive_scan(cnt, warp_sums, &tot);
+        __syncthreads();
+        int32_t tiles = 0;
+        for (int32_t i = base + (tid - base & (kSchedThreads - 1)); i < base + tot && i < max_units; i += kSchedThreads) {
+            const int32_t at = last_at_most(off, i - base);
+            const pcp_row_t r = a.rows[r0 + at];
+            const PackedUnit x = packed_unit(a, r.req, r.q_start, r.q_len, r.kv_end - r.q_len, i - base - off[at], span,
+                                             lo_of[at], r.kv_end, grp_of[at] >= 0 ? a.nparts : 0);
+            put(i, x);
+            tiles += (x.k_end + kBlockN - 1) / kBlockN;
+        }
+        if (tiles) atomicAdd(&cost[3], tiles);
+        if (tid == 0) cost[2] += tot;
         if (ng > 0)  // a warp per unit
             for (int32_t u = warp; u < tot; u += kSchedThreads / 32) {
-                const int32_t i = last_at_most(off, kSchedThreads, u);
-                if (row_grp[r0 + i] < 0) continue;
-                const pcp_row_t row = a.rows[r0 + i];
-                const int32_t t1 = min(row.q_len, (u - off[i] + 1) * span);
-                const MergeTask m{r0 + i, 0, 0, grp_shards[row_grp[r0 + i]]};
-                for (int32_t t = (u - off[i]) * span + lane; t < t1; t += 32) merge[row.q_start + t] = m;
+                const int32_t at = last_at_most(off, u);
+                if (grp_of[at] < 0) continue;
+                const pcp_row_t r = a.rows[r0 + at];
+                const int32_t t1 = min(r.q_len, (u - off[at] + 1) * span);
+                const MergeTask m{r0 + at, 0, 0, shards_of[grp_of[at]]};
+                for (int32_t t = (u - off[at]) * span + lane; t < t1; t += 32) merge[r.q_start + t] = m;
             }
         base += tot;
-        __syncthreads();  // off is rewritten
+        __syncthreads();  // off, lo_of and grp_of are rewritten
     }
     // The SMs of the decode rows and the prefixes' shards: lane n - 1 of warp 0 models n
     // shards. SM times measured on GB300 (us): a decode item 1 and a 128-key tile 0.95
@@ -1520,10 +1538,10 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         float items = (float)cost[2], tiles = (float)cost[3];
         int32_t longest = 0;
         for (int32_t g = 0; g < ng; ++g) {
-            if (grp_shards[g] == 0) continue;
-            const pcp_prefix_t p = a.prefixes[g];
+            if (shards_of[g] == 0) continue;
+            const pcp_prefix_t p = prefix[g];
             const int32_t t = (p.prefix_len + kBlockN - 1) / kBlockN, tok = (p.q_len + span - 1) / span;
-            const int32_t n = min(lane + 1, grp_shards[g]);
+            const int32_t n = min(lane + 1, shards_of[g]);
             items += (float)(tok * n);
             tiles += (float)tok * t;
             longest = max(longest, (t + n - 1) / n);
@@ -1544,27 +1562,33 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         const int pick = __ffs(__ballot_sync(0xffffffffu, us == best)) - 1;
         if (lane == pick) {
             max_shards = lane + 1;
+            header[1] = num_rows <= kDecTcMaxRows ? cost[0] * a.hkv : 0;
             header[2] = k > 0 ? k : nsm;
             header[3] = nsm - k;
+            header[4] = lane + 1;
+        }
+        // first place of each length in the decode list
+        if (lane == 0) {
+            int32_t t = 0;
+            for (int b = kTailBuckets; b >= 1; --b) {
+                tail_off[b] = t;
+                t += tail_cnt[b];
+            }
+            tail_off[0] = 0;
         }
     }
     __syncthreads();
-    for (int32_t g = threadIdx.x; g < ng; g += kSchedThreads) grp_shards[g] = min(grp_shards[g], max_shards);
-    for (int32_t t = threadIdx.x; t < a.total_q && ng > 0; t += kSchedThreads)
-        merge[t].shards = min(merge[t].shards, max_shards);
-    __syncthreads();
-    for (int32_t g0 = 0; g0 < ng; g0 += kSchedThreads) {
-        const int32_t g = g0 + threadIdx.x;
+    if (ng > 0) {
         int32_t cnt = 0;
-        if (g < ng) cnt = grp_shards[g] * ((a.prefixes[g].q_len + span - 1) / span);
+        if (tid < ng) cnt = min(shards_of[tid], max_shards) * ((prefix[tid].q_len + span - 1) / span);
         int32_t tot;
-        off[threadIdx.x] = block_exclusive_scan(cnt, warp_sums, &tot);
+        off[tid] = block_exclusive_scan(cnt, warp_sums, &tot);
         __syncthreads();
-        for (int32_t u = threadIdx.x; u < tot && base + u < max_units; u += kSchedThreads) {
-            const int32_t i = last_at_most(off, kSchedThreads, u);
-            const pcp_prefix_t p = a.prefixes[g0 + i];
-            const int32_t shards = grp_shards[g0 + i], pages = (p.prefix_len + bs - 1) / bs;
-            const int32_t sh = (u - off[i]) % shards, mt = (u - off[i]) / shards;
+        for (int32_t i = base + (tid - base & (kSchedThreads - 1)); i < base + tot && i < max_units; i += kSchedThreads) {
+            const int32_t at = last_at_most(off, i - base), u = i - base - off[at];
+            const pcp_prefix_t p = prefix[at];
+            const int32_t shards = min(shards_of[at], max_shards), pages = (p.prefix_len + bs - 1) / bs;
+            const int32_t sh = u % shards, mt = u / shards;
             const int32_t k_lo = (int32_t)((int64_t)pages * sh / shards) * bs;
             const int32_t k_hi = (int32_t)min((int64_t)p.prefix_len, (int64_t)pages * (sh + 1) / shards * bs);
             PackedUnit x = packed_unit(a, p.req, p.q_start, p.q_len, 0, mt, span, k_lo, k_hi, 1 + sh);
@@ -1572,46 +1596,60 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
             x.k_lo = k_lo;
             x.shift = k_lo;
             x.k_end = k_hi - k_lo;
-            units[base + u] = x;
-            atomicAdd(&classes[class_of(x)], 1);
+            put(i, x);
         }
         base += tot;
         __syncthreads();
     }
     const int32_t n = (int32_t)min((int64_t)base, max_units);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        int32_t t = 0;
-        for (int b = kTailBuckets; b >= 1; --b) {
-            tail_off[b] = t;
-            t += tail_cnt[b];
+    if (tid == 0) header[0] = n;
+    if (n > 0) {
+        // longest first (units of one class in any order: an item writes only its own
+        // results, which do not depend on its place)
+        int32_t tot;
+        const int32_t first = block_exclusive_scan(classes[tid], warp_sums, &tot);
+        classes[tid] = first;
+        __syncthreads();
+        for (int32_t i = tid; i < n; i += kSchedThreads) {
+            const PackedUnit x = i < kSchedThreads ? mine : units[i];
+            sorted[atomicAdd(&classes[class_of(x)], 1)] = x;
         }
-        tail_off[0] = 0;
-        header[0] = n;
-        header[1] = dbase + t * a.hkv;
-        dec_pre[num_rows] = dbase;
+        __syncthreads();  // off is rewritten
     }
-    __syncthreads();
-    for (int32_t r0 = 0; r0 < num_rows; r0 += kSchedThreads) {
-        const int32_t ri = r0 + threadIdx.x;
-        int32_t b = 0;
-        if (ri < num_rows && row_ok[ri]) {
-            const pcp_row_t row = a.rows[ri];
-            if (row.q_len == 1) b = (key_range(a, row, row_lo[ri]).len % a.chunk + kBlockN - 1) / kBlockN;
-        }
-        const int32_t at = tail_place(b, tail_off, tail_fill, tail_warp);
-        if (b) dec_pre[num_rows + 1 + at] = ri;
-    }
-    if (n == 0) return;
-    // longest first (units of one class in any order: an item writes only its own
-    // results, which do not depend on its place)
+    if (cost[0] == 0 || num_rows > kDecTcMaxRows) return;
+    // the decode splits, by a search over the rows' running counts
     int32_t tot;
-    const int32_t first = block_exclusive_scan(classes[threadIdx.x], warp_sums, &tot);
-    classes[threadIdx.x] = first;
+    const int32_t first = block_exclusive_scan(my_splits, warp_sums, &tot);
+    off[tid] = first;
+    // the rows' fields, in the shared memory of the counting pass and the groups
+    int32_t* len_of = classes;
+    int4* row_of = reinterpret_cast<int4*>(prefix);  // request, token, first own key, kv_end
     __syncthreads();
-    for (int32_t i = threadIdx.x; i < n; i += kSchedThreads) {
-        const PackedUnit x = units[i];
-        sorted[atomicAdd(&classes[class_of(x)], 1)] = x;
+    len_of[tid] = my_len;
+    row_of[tid] = make_int4(row.req, row.q_start, my_lo, row.kv_end);
+    __syncthreads();
+    for (int32_t i0 = 0; i0 < tot; i0 += kSchedThreads) {
+        const int32_t i = i0 + tid;
+        DecUnit x{};
+        int32_t b = 0;
+        if (i < tot) {
+            const int32_t at = last_at_most(off, i);
+            const int4 fields = row_of[at];
+            pcp_row_t r{};
+            r.kv_end = fields.w;
+            const KeyRange kr = key_range(a, r, fields.z);
+            x.row = at;
+            x.req = fields.x;
+            x.q_start = fields.y;
+            x.lo = (i - off[at]) * a.chunk;
+            x.hi = min(len_of[at], x.lo + a.chunk);
+            x.sinks = kr.sinks;
+            x.gap_end = kr.lo - kr.shift;
+            x.shift = kr.shift;
+            b = (x.hi - x.lo + kBlockN - 1) / kBlockN;
+        }
+        const int32_t to = tail_place(b, tail_off, tail_fill, tail_warp);
+        if (b) dec_units[to] = x;
     }
 }
 
@@ -1715,10 +1753,10 @@ int launch_schedule(const PrefillArgs& a, int32_t flags, Unit* units, Unit* unit
 }
 
 int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header,
-                          int32_t* row_ok, int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, MergeTask* merge,
-                          int32_t* dec_pre, int64_t max_units, cudaStream_t stream) {
-    range_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(a, units, units_sorted, header, row_ok, row_lo, row_grp,
-                                                           grp_shards, merge, dec_pre, max_units);
+                          int32_t* row_ok, int32_t* row_lo, MergeTask* merge, DecUnit* dec_units, int64_t max_units,
+                          cudaStream_t stream) {
+    range_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(a, units, units_sorted, header, row_ok, row_lo, merge,
+                                                           dec_units, max_units);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;

@@ -39,13 +39,21 @@ struct alignas(16) PackedUnit {
     int32_t shift, k_end;  // slots of the walk: key = slot + shift past the sinks; its length
 };
 
+// A split of a one-token row in those calls' decode list; items are splits x kv
+// heads. Slots [sinks, gap_end) of the row's walk (KeyRange) hold keys that it does not see.
+struct alignas(16) DecUnit {
+    int32_t row, req, q_start;
+    int32_t lo, hi;  // slots
+    int32_t sinks, gap_end, shift;
+};
+
 // What makes up the result of a token (shared-prefix calls; indexed by token) or
 // of a one-token row (window calls; by row): row is -1 where the merge has
 // nothing to do.
 struct alignas(16) MergeTask {
     int32_t row, token;  // token: of a one-token row (a longer row's tokens are their index)
     int32_t splits;      // decode splits of a one-token row; 0: a longer row, its own keys in one partial
-    int32_t shards;      // of its group's prefix
+    int32_t shards;      // of its group's prefix, at most header[4] of them
 };
 
 // Workspace layout of pcp_attn_varlen (all offsets 256-byte aligned).
@@ -127,6 +135,7 @@ struct PrefillArgs {
     int32_t overlap;            // the decode kernel is the persistent one: it can share the SMs
     int32_t direct;             // decode rows have one partial each: written straight to out and lse
     int32_t slots;              // token tiles per packed item: 1 or 2
+    const DecUnit* dec_units;   // the decode list, longest first
     const PackedUnit* packed;   // the packed work list, longest first
     const int32_t* row_lo;      // first own key of each row (0, or its group's prefix length)
     const pcp_prefix_t* prefixes;
@@ -228,8 +237,8 @@ int launch_separate_merge(const PrefillArgs& a, cudaStream_t stream);
 // Window and shared-prefix calls: the schedule, the packed kernel over its work
 // list, the decode partials (decode_parts per split) and their merge.
 int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header,
-                          int32_t* row_ok, int32_t* row_lo, int32_t* row_grp, int32_t* grp_shards, MergeTask* merge,
-                          int32_t* dec_pre, int64_t max_units, cudaStream_t stream);
+                          int32_t* row_ok, int32_t* row_lo, MergeTask* merge, DecUnit* dec_units, int64_t max_units,
+                          cudaStream_t stream);
 int launch_packed(const PrefillArgs& a, cudaStream_t stream);
 int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                         cudaStream_t stream);

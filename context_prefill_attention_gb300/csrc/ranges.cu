@@ -19,7 +19,7 @@ constexpr int kMaxPrefixes = 1024;
 constexpr int kMaxShards = 32;     // shards of a prefix
 
 struct RangeLayout {
-    size_t header, row_ok, row_lo, row_grp, grp_shards, merge, dec_pre, units, units_sorted, part_out, part_lse, dec_out,
+    size_t header, row_ok, row_lo, merge, dec_units, units, units_sorted, part_out, part_lse, dec_out,
         dec_lse, total;
     int64_t max_units;
     int32_t slots, chunk, max_splits, nparts;
@@ -79,10 +79,8 @@ RangeLayout range_layout(int32_t num_rows, int32_t num_prefixes, int32_t total_q
     w.header = take(64 * sizeof(int32_t));
     w.row_ok = take((size_t)num_rows * 4);
     w.row_lo = take((size_t)num_rows * 4);
-    w.row_grp = take((size_t)num_rows * 4);
-    w.grp_shards = take((size_t)ng * 4);
     w.merge = take((size_t)(ng > 0 ? total_q : num_rows) * sizeof(MergeTask));
-    w.dec_pre = take((2 * (size_t)num_rows + 1) * 4);
+    w.dec_units = take(num_rows <= kDecTcMaxRows ? (size_t)num_rows * w.max_splits * sizeof(DecUnit) : 0);
     w.units = take((size_t)w.max_units * sizeof(PackedUnit));
     w.units_sorted = take((size_t)w.max_units * sizeof(PackedUnit));
     w.part_out = take((size_t)w.nparts * total_q * hq * d * 4);
@@ -183,7 +181,7 @@ int range_call(const RangeCall& c) {
     a.row_ok = ints(w.row_ok);
     a.packed = reinterpret_cast<const PackedUnit*>(ws + w.units_sorted);
     a.num_units = ints(w.header);
-    a.dec_pre = ints(w.dec_pre);
+    a.dec_units = reinterpret_cast<const DecUnit*>(ws + w.dec_units);
     a.status = c.status;
     a.k_descale = c.fp8 ? c.k_descale : nullptr;
     a.v_descale = c.fp8 ? c.v_descale : nullptr;
@@ -202,8 +200,8 @@ int range_call(const RangeCall& c) {
     MergeTask* tasks = reinterpret_cast<MergeTask*>(ws + w.merge);
     int rc = launch_range_schedule(a, reinterpret_cast<PackedUnit*>(ws + w.units),
                                    reinterpret_cast<PackedUnit*>(ws + w.units_sorted), ints(w.header), ints(w.row_ok),
-                                   ints(w.row_lo), ints(w.row_grp), ints(w.grp_shards), tasks, ints(w.dec_pre),
-                                   w.max_units, c.stream);
+                                   ints(w.row_lo), tasks, reinterpret_cast<DecUnit*>(ws + w.dec_units), w.max_units,
+                                   c.stream);
     if (rc != PCP_OK) return rc;
     float* dec_out = reinterpret_cast<float*>(ws + w.dec_out);
     float* dec_lse = reinterpret_cast<float*>(ws + w.dec_lse);
