@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kDecThreads)
             if (d == 0) a.lse[(size_t)h * a.total_q + t] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
             continue;
         }
-        const size_t slot = ((size_t)ri * a.hq + h) * (2 * max_splits) + split;  // one partial per split
+        const size_t slot = ((size_t)ri * a.hq + h) * (RNG ? max_splits : 2 * max_splits) + split;
         dec_out[slot * D + d] = L > 0.f ? O / L * vd : 0.f;
         if (d == 0) dec_lse[slot] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
     }
@@ -453,9 +453,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // Merge of a window or shared-prefix call: the results of every token that has
-// partials, by log-sum-exp, into out (bf16) and lse. A row of one token has
-// parts_per_split partials for each split of its own keys; a longer row of a
-// prefix group one for its own keys (partial nparts - 1 of part_out); the rows of
+// partials, by log-sum-exp, into out (bf16) and lse. A row of one token has one
+// partial for each split of its own keys; a longer row of a prefix group one for its own keys (partial nparts - 1 of part_out); the rows of
 // a group also those of the prefix's shards (partials 0 .. shards - 1). A longer
 // row outside every group was written by the packed kernel.
 //
@@ -467,7 +466,7 @@ constexpr int kMergeBatch = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
     range_merge_kernel(PrefillArgs a, const MergeTask* __restrict__ tasks, const float* __restrict__ dec_out,
-                       const float* __restrict__ dec_lse, int max_splits, int parts_per_split) {
+                       const float* __restrict__ dec_lse, int max_splits) {
     constexpr int kV = D / 32;
     using Vec = typename std::conditional<kV == 4, float4, float2>::type;
     grid_wait();
@@ -481,8 +480,8 @@ __global__ void __launch_bounds__(256)
     const bool one = task.splits > 0;
     const int32_t t = one ? task.token : at;
     // partials 0 .. n - 1 are the row's own keys', the others the prefix's shards
-    const int n = one ? parts_per_split * task.splits : 1, all = n + task.shards;
-    const size_t base = ((size_t)task.row * a.hq + h) * (2 * max_splits);
+    const int n = one ? task.splits : 1, all = n + task.shards;
+    const size_t base = ((size_t)task.row * a.hq + h) * max_splits;
     const size_t out_stride = (size_t)a.total_q * a.hq * D, lse_stride = (size_t)a.hq * a.total_q;
     const size_t li = (size_t)h * a.total_q + t, o = ((size_t)t * a.hq + h) * D;
     float M = -INFINITY, W = 0.f, O[kV] = {};
@@ -589,49 +588,48 @@ int launch_decode_d(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_
 #define PCP_DECODE_TC 1  // 1: the tensor-core decode where it applies (head_dim 128, G <= 8)
 #endif
 
-// the tensor-core kernel writes a partial per softmax warpgroup over an FP8 cache and
-// with more than 8 q heads per kv head
-int decode_parts(const PrefillArgs& a) {
-    return PCP_DECODE_TC && decode_tc_applies(a) && (a.k_descale || a.hq / a.hkv > 8) ? 2 : 1;
-}
-
 bool decode_side_applies(const PrefillArgs& a) { return PCP_DECODE_TC && decode_tc_applies(a); }
 
 namespace {
 
-// The decode partials of every decode row (decode_parts per split).
-int launch_decode_parts(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
-                        cudaStream_t stream, int grid) {
-    if (a.d != 64 && a.d != 128) return PCP_ERR_UNSUPPORTED;
-    int rc = PCP_DECODE_TC ? launch_decode_tc(a, dec_out, dec_lse, max_splits, stream, grid) : PCP_ERR_UNSUPPORTED;
-    if (rc == PCP_ERR_UNSUPPORTED)
-        rc = a.d == 64 ? launch_decode_d<64>(a, dec_out, dec_lse, max_splits, stream)
-                       : launch_decode_d<128>(a, dec_out, dec_lse, max_splits, stream);
-    return rc;
+int launch_decode_cuda_cores(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
+                             cudaStream_t stream) {
+    return a.d == 64 ? launch_decode_d<64>(a, dec_out, dec_lse, max_splits, stream)
+                     : launch_decode_d<128>(a, dec_out, dec_lse, max_splits, stream);
 }
 
 }  // namespace
 
 int launch_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                   cudaStream_t stream, int grid) {
-    const int rc = launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (a.d != 64 && a.d != 128) return PCP_ERR_UNSUPPORTED;
+    int rc = PCP_DECODE_TC ? launch_decode_tc(a, dec_out, dec_lse, max_splits, stream, grid) : PCP_ERR_UNSUPPORTED;
+    // partials per split: the tensor-core kernel writes one per softmax warpgroup
+    // over an FP8 cache and with more than 8 q heads per kv head
+    int pps = (a.k_descale || a.hq / a.hkv > 8) ? 2 : 1;
+    if (rc == PCP_ERR_UNSUPPORTED) {
+        rc = launch_decode_cuda_cores(a, dec_out, dec_lse, max_splits, stream);
+        pps = 1;
+    }
     if (rc != PCP_OK) return rc;
-    return launch_merge(a, dec_out, dec_lse, max_splits, decode_parts(a), stream);
+    return launch_merge(a, dec_out, dec_lse, max_splits, pps, stream);
 }
 
 int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                         cudaStream_t stream) {
-    return launch_decode_parts(a, dec_out, dec_lse, max_splits, stream, 0);
+    if (a.d != 64 && a.d != 128) return PCP_ERR_UNSUPPORTED;
+    const int rc = launch_decode_pair(a, dec_out, dec_lse, max_splits, stream);
+    return rc == PCP_ERR_UNSUPPORTED ? launch_decode_cuda_cores(a, dec_out, dec_lse, max_splits, stream) : rc;
 }
 
 int launch_range_merge(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out, const float* dec_lse,
-                       int32_t max_splits, int parts, cudaStream_t stream) {
+                       int32_t max_splits, cudaStream_t stream) {
     const int64_t jobs = (int64_t)(a.num_prefixes > 0 ? a.total_q : a.num_rows) * a.hq;
     const dim3 grid((unsigned)((jobs + 7) / 8));
     const cudaError_t e = a.d == 64 ? launch_chained(range_merge_kernel<64>, grid, dim3(256), 0, stream, a, tasks, dec_out,
-                                                     dec_lse, max_splits, parts)
+                                                     dec_lse, max_splits)
                                     : launch_chained(range_merge_kernel<128>, grid, dim3(256), 0, stream, a, tasks,
-                                                     dec_out, dec_lse, max_splits, parts);
+                                                     dec_out, dec_lse, max_splits);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }

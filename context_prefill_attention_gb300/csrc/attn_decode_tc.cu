@@ -62,30 +62,13 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "decode_tc_parts.cuh"
 #include "pcp_device.cuh"
 #include "pcp_internal.h"
 
 namespace pcp {
 
 namespace {
-
-constexpr int kD = 128;          // head_dim this kernel takes
-constexpr int kKeys = 128;       // keys per tile: the M of S^T
-constexpr int kN = 16;           // the N of S^T (and of O^T up to 8 q heads per kv head)
-constexpr int kMaxG = 16;        // q heads per kv head (FP8: 8)
-constexpr int kTerms = 2;        // FP8: e4m3 terms per q element (their sum is the bf16 q exactly)
-constexpr int kProdWarp = 8;     // warp 8: K tiles and Q^T; warp 9: V tiles
-constexpr int kMmaWarp = 10;     // lane 0 issues the S MMAs (the warp owns the TMEM allocation)
-constexpr int kPvWarp = 11;      // lane 0 issues the PV MMAs
-constexpr int kConvWarp0 = 12;
-constexpr int kConvThreads = 128;  // FP8: threads widening one V tile (one or two such sets)
-// FP8 converter warps: two sets of four taking alternate V tiles where the
-// softmax fits the registers that 20 warps leave (G <= 4), else one set
-__host__ __device__ constexpr int conv_warps(bool f8, int gp) { return f8 ? (gp <= 4 ? 8 : 4) : 0; }
-__host__ __device__ constexpr int tc_threads(bool f8, int gp) { return 32 * (12 + conv_warps(f8, gp)); }
-constexpr int kMaxPages = kDecodeChunk / 8;  // block-table entries of one split (block_size >= 8)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <bool F8, int GP>
 struct TcCfg {
@@ -140,9 +123,6 @@ static_assert(TcCfg<true, 4>::kQC % 1024 == 0 && TcCfg<true, 8>::kP % 1024 == 0 
 
 struct DecItem {
     int32_t ri, req, q_start, hk, split, lo, hi, nt;
-    int32_t sinks, gap_end, shift;  // RNG (DecUnit): lo and hi count slots of the row's walk
-    // RNG: whether slot v holds a key that the row sees
-    __device__ __forceinline__ bool live(int32_t v) const { return v < sinks || v >= gap_end; }
 };
 
 // Item p of the decode work list: first every full kDecodeChunk-key split (row
@@ -151,49 +131,29 @@ struct DecItem {
 // in the order of tail_rows (longest partial first). Dealt in snake order, the
 // CTAs then end within a fraction of a split of each other. The caller's items
 // rise, so the row cursor ri only walks forward over the prefix.
-// RNG (window and shared-prefix calls): the scheduler's list holds the splits
-// themselves, longest first.
-template <bool RNG>
-__device__ __forceinline__ DecItem dec_item(const int32_t* pre, int32_t& ri, int32_t p, const PrefillArgs& a,
-                                            const int32_t* tail_rows) {
-    const int32_t num_rows = a.num_rows, hkv = a.hkv;
-    DecItem it{};
-    if constexpr (RNG) {
-        const int32_t n = p / hkv;
-        const int4* src = reinterpret_cast<const int4*>(a.dec_units + n);
-        const int4 x = src[0], y = src[1];
-        it.ri = x.x;
-        it.req = x.y;
-        it.q_start = x.z;
-        it.hk = p - n * hkv;
-        it.lo = x.w;
-        it.hi = y.x;
-        it.split = it.lo / a.chunk;
-        it.sinks = y.y;
-        it.gap_end = y.z;
-        it.shift = y.w;
+__device__ __forceinline__ DecItem dec_item(const int32_t* pre, int32_t& ri, int32_t p, const pcp_row_t* rows,
+                                            const int32_t* tail_rows, int32_t num_rows, int32_t hkv) {
+    const int32_t nfull = pre[num_rows];
+    const bool full = p < nfull;
+    int32_t r, rem;
+    if (full) {
+        while (pre[ri + 1] <= p) ++ri;
+        r = ri;
+        rem = p - pre[r];
     } else {
-        const int32_t nfull = pre[num_rows];
-        const bool full = p < nfull;
-        int32_t r, rem;
-        if (full) {
-            while (pre[ri + 1] <= p) ++ri;
-            r = ri;
-            rem = p - pre[r];
-        } else {
-            rem = p - nfull;
-            r = tail_rows[rem / hkv];
-        }
-        const pcp_row_t row = a.rows[r];
-        const int32_t nf = row.kv_end / kDecodeChunk;  // full splits of the row (>= 1 on the full side)
-        it.ri = r;
-        it.req = row.req;
-        it.q_start = row.q_start;
-        it.hk = full ? rem / nf : rem % hkv;
-        it.split = full ? rem % nf : nf;
-        it.lo = it.split * kDecodeChunk;
-        it.hi = min(row.kv_end, it.lo + kDecodeChunk);
+        rem = p - nfull;
+        r = tail_rows[rem / hkv];
     }
+    const pcp_row_t row = rows[r];
+    const int32_t nf = row.kv_end / kDecodeChunk;  // full splits of the row (>= 1 on the full side)
+    DecItem it;
+    it.ri = r;
+    it.req = row.req;
+    it.q_start = row.q_start;
+    it.hk = full ? rem / nf : rem % hkv;
+    it.split = full ? rem % nf : nf;
+    it.lo = it.split * kDecodeChunk;
+    it.hi = min(row.kv_end, it.lo + kDecodeChunk);
     it.nt = (it.hi - it.lo + kKeys - 1) / kKeys;
     return it;
 }
@@ -212,174 +172,15 @@ __device__ __forceinline__ bool bar_all_or(bool pred) {
     return r != 0;
 }
 
-// Named barrier `id` over `n` threads (whole warps).
-__device__ __forceinline__ void bar_sync_named(int id, int n) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
-// Named barrier `id` over one softmax warpgroup (128 threads) that also ORs a
-// predicate: every thread gets the same answer, so the warps leave their loops
-// together.
-__device__ __forceinline__ bool bar_wg_or(int id, bool pred) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)pred), "r"(id)
-        : "memory");
-    return r != 0;
-}
-
-// Max (kMax) or sum over the warp of GP values per lane, by reduce-scatter: each
-// step with offset o = 16, 8, ... halves the values a lane keeps (the upper half
-// where bit o of the lane is set), the remaining offsets reduce the last one.
-// Lane l ends with head l / (32 / GP) reduced over all 32 lanes.
-template <int GP, bool kMax>
-__device__ __forceinline__ float warp_scatter(const float (&x)[GP], int lane) {
-    float v[GP];
-#pragma unroll
-    for (int h = 0; h < GP; ++h) v[h] = x[h];
-#pragma unroll
-    for (int o = 16, n = GP; n > 1; o >>= 1, n >>= 1) {
-        const bool upper = (lane & o) != 0;
-#pragma unroll
-        for (int k = 0; k < n / 2; ++k) {
-            const float send = upper ? v[k] : v[k + n / 2];
-            const float keep = upper ? v[k + n / 2] : v[k];
-            const float r = __shfl_xor_sync(0xffffffffu, send, o);
-            v[k] = kMax ? fmaxf(keep, r) : keep + r;
-        }
-    }
-#pragma unroll
-    for (int o = 16 / GP; o >= 1; o >>= 1) {
-        const float r = __shfl_xor_sync(0xffffffffu, v[0], o);
-        v[0] = kMax ? fmaxf(v[0], r) : v[0] + r;
-    }
-    return v[0];
-}
-
-// One tile of FP8 codes -> f16 in the 128-byte-swizzled K-major layout of a
-// stage (dims 64h..64h+63 of row r in half h, 16-byte chunk c of that row at
-// chunk c ^ (r & 7)). The codes of row r (128 bytes) sit where half 1 of row r
-// goes; the eight threads of a row are in one warp and all load before any of
-// them stores. Rows at or past nvalid are written as zeros (their codes may be
-// stale or unwritten cache slots). Run by the 128 converter threads.
-// live(r): further rows for which it is false are written as zeros too.
-template <typename Live>
-__device__ __forceinline__ void widen_tile(uint8_t* tile, int nvalid, int ct, Live live) {
-    constexpr int kHalf = kKeys * 128;
-    constexpr int kRpp = kConvThreads / 8;  // rows per pass
-    constexpr int kBatch = 4;
-    const int t = ct % 8, rsub = ct / 8;
-    const int h = t / 4, c0 = 2 * (t % 4);
-    // threads of the second half store their odd chunk first, so the eight
-    // threads of a row hit eight different bank groups in each store
-    const int first = c0 + (t >= 4 ? 1 : 0), second = c0 + (t >= 4 ? 0 : 1);
-    const uint8_t* codes = tile + kHalf;
-#pragma unroll 1
-    for (int r0 = 0; r0 < kKeys; r0 += kRpp * kBatch) {
-        uint4 c[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + kRpp * b + rsub;
-            c[b] = r < nvalid && live(r) ? *reinterpret_cast<const uint4*>(codes + r * kD + 16 * t)
-                                         : make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + kRpp * b + rsub;
-            const uint2 w0 = e4m3x4_to_f16x4(c[b].x), w1 = e4m3x4_to_f16x4(c[b].y);
-            const uint2 w2 = e4m3x4_to_f16x4(c[b].z), w3 = e4m3x4_to_f16x4(c[b].w);
-            const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y);  // dims 16t .. 16t+7
-            const uint4 hi = make_uint4(w2.x, w2.y, w3.x, w3.y);  // dims 16t+8 .. 16t+15
-            uint8_t* row = tile + h * kHalf + r * 128;
-            const bool lo_first = first == c0;
-            *reinterpret_cast<uint4*>(row + ((first ^ (r & 7)) << 4)) = lo_first ? lo : hi;
-            *reinterpret_cast<uint4*>(row + ((second ^ (r & 7)) << 4)) = lo_first ? hi : lo;
-        }
-        __syncwarp();
-    }
-}
-
-// FP8: the group's q heads as kTerms e4m3 terms each. Input: the bf16 Q^T
-// tile as TMA wrote it (two 64-dim halves of 16 rows, 128-byte swizzled).
-// Output: the swizzled K-major layout of an e4m3 MMA operand, row t * GP + h
-// holding term t of head h (128 codes, 16-byte chunk c of row r at chunk
-// c ^ (r & 7)). Head h is first scaled by 2^(8 - ex), ex the binary exponent
-// of its largest magnitude (frexp), so that every element lies below 256. The
-// first term is the e4m3 rounding of the scaled element x (4 significant bits);
-// the remainder x - term is a multiple of x's last bit no larger than 8 of
-// them (x has 8 significant bits), so it is an e4m3 value too and the two
-// terms sum to x exactly, unless the remainder falls under e4m3's smallest
-// subnormal (2^-9 of the scaled unit, where the largest element lies in
-// [128, 256): only elements below 2^-9 of the head's largest can lose bits, at
-// most 2^-17 of it). qscale[h] = 2^(ex - 8) undoes
-// the scaling. Warp w of the converter set does heads w and w + 4, lane l dims
-// 4l .. 4l + 3. Returns whether an element of one of the G real heads lies
-// beyond +-65504 (reported as PCP_ERR_RANGE, as the prefill rows' q is).
-template <int GP>
-__device__ __forceinline__ bool q_to_e4m3_terms(const uint8_t* qbf, uint8_t* qc, float* qscale, int w, int lane,
-                                                int G) {
-    bool over = false;
-#pragma unroll
-    for (int h = w; h < GP; h += 4) {
-        const int d = 4 * lane, half = d >> 6, col = d & 63;
-        const uint2 raw =
-            *reinterpret_cast<const uint2*>(qbf + half * (kN * 128) + h * 128 + (((col >> 3) ^ (h & 7)) << 4) + (col & 7) * 2);
-        float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
-                      __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u)};
-        float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        over |= h < G && m > 65504.f;
-        int ex = 0;
-        frexpf(m, &ex);
-        const float f = ldexpf(1.f, 8 - ex);
-        if (lane == 0) qscale[h] = ldexpf(1.f, ex - 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= f;
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t) {
-            const uint32_t codes = f32x2_to_e4m3x2(x[0], x[1]) | (f32x2_to_e4m3x2(x[2], x[3]) << 16);
-            const int row = t * GP + h;
-            *reinterpret_cast<uint32_t*>(qc + row * 128 + (((d >> 4) ^ (row & 7)) << 4) + (d & 15)) = codes;
-            if (t + 1 < kTerms) {
-                float back[4];
-                e4m3x4_to_f32(codes, back);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] -= back[e];  // exact: both hold few significant bits
-            }
-        }
-    }
-    return over;
-}
-
-template <bool F8>
-__device__ __forceinline__ uint16_t to16(float x) {
-    if constexpr (F8) return __half_as_ushort(__float2half_rn(x));
-    return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-template <bool F8>
-__device__ __forceinline__ float from16(uint16_t x) {
-    if constexpr (F8) return __half2float(__ushort_as_half(x));
-    return __bfloat162float(__ushort_as_bfloat16(x));
-}
-
-// RNG: the rows' own key ranges (window and shared-prefix calls).
-template <bool F8, int GP, bool RNG>
+template <bool F8, int GP>
 __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, PrefillArgs a, float* __restrict__ dec_out,
                      float* __restrict__ dec_lse, int max_splits, int q_rows) {
     using C = TcCfg<F8, GP>;
     constexpr int kKS = C::kKS, kVS = C::kVS, kNS = C::kNS;
-    if constexpr (!RNG) {
-        if ((int32_t)blockIdx.x >= a.num_units[1]) return;
-    }
+    const int32_t total = a.num_units[1];
+    if ((int32_t)blockIdx.x >= total) return;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -416,8 +217,16 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int G = a.hq / a.hkv;
     const int32_t bs = a.block_size;
+    const int32_t step = (int32_t)gridDim.x;
+    // item of this CTA in round rd: snake order (forward on even rounds, backward
+    // on odd ones) over the list, whose full splits come first and partial ones
+    // longest first
+    auto item_of_round = [&](int32_t rd) -> int32_t {
+        return rd * step + ((rd & 1) ? step - 1 - (int32_t)blockIdx.x : (int32_t)blockIdx.x);
+    };
     const int32_t* tail_rows = a.dec_pre + a.num_rows + 1;
 
+    for (int i = threadIdx.x; i <= a.num_rows; i += tc_threads(F8, GP)) pre[i] = a.dec_pre[i];
     if (threadIdx.x == 0) {
         const uint32_t filled = F8 ? 4 : 1;  // FP8: each warp of the converter set arrives
         for (int s = 0; s < kKS; ++s) {
@@ -451,23 +260,6 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    // RNG: launched behind the scheduler, whose work list is read from here on
-    if constexpr (RNG) {
-        grid_wait();
-        grid_launch_dependents();
-    }
-    if constexpr (!RNG)
-        for (int i = threadIdx.x; i <= a.num_rows; i += tc_threads(F8, GP)) pre[i] = a.dec_pre[i];
-    // CTAs that take items: all of them, or (RNG) as many as the scheduler gave the
-    // decode rows beside the packed kernel's
-    const int32_t step = RNG ? a.num_units[2] : (int32_t)gridDim.x;
-    const int32_t total = !RNG || (int32_t)blockIdx.x < step ? a.num_units[1] : 0;
-    // item of this CTA in round rd: snake order (forward on even rounds, backward
-    // on odd ones) over the list, whose full splits come first and partial ones
-    // longest first
-    auto item_of_round = [&](int32_t rd) -> int32_t {
-        return rd * step + ((rd & 1) ? step - 1 - (int32_t)blockIdx.x : (int32_t)blockIdx.x);
-    };
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -492,7 +284,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         int32_t ri = 0;
         bool ok = true;
         for (int32_t rd = 0, p = item_of_round(0); p < total && ok; p = item_of_round(++rd)) {
-            const DecItem it = dec_item<RNG>(pre, ri, p, a, tail_rows);
+            const DecItem it = dec_item(pre, ri, p, a.rows, tail_rows, a.num_rows, a.hkv);
             // the split's block-table entries as first cache rows; a bad id maps to a
             // row past the cache (zero filled) and reports PCP_ERR_RANGE
             const int32_t* table = a.block_table + (size_t)it.req * a.max_blocks;
@@ -500,8 +292,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
             const int npg = (it.hi - it.lo + bs - 1) / bs;
             __syncwarp();
             for (int i = lane; i < npg; i += 32) {
-                int32_t pg = pg0 + i;
-                if (RNG && pg * bs >= it.sinks) pg += it.shift / bs;  // (a page begun by sinks holds them)
+                const int32_t pg = pg0 + i;
                 const int32_t id = pg < a.max_blocks ? __ldg(table + pg) : -1;
                 int32_t y = oob;
                 if (id >= 0 && id < a.num_blocks) y = id * bs;
@@ -577,7 +368,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
             bool ok = true;
             const bool s_role = warp == kMmaWarp;
             for (int32_t rd = 0, p = item_of_round(0); p < total && ok; p = item_of_round(++rd)) {
-                const DecItem it = dec_item<RNG>(pre, ri, p, a, tail_rows);
+                const DecItem it = dec_item(pre, ri, p, a.rows, tail_rows, a.num_rows, a.hkv);
                 const int qb = ic & 1;
                 if (s_role && !(ok = mbar_wait(q_full(qb), (ic >> 1) & 1, abort_flag))) break;
                 for (int j = 0; j < it.nt; ++j, ++g) {
@@ -641,7 +432,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         int32_t ri = 0;
         bool ok = true;
         for (int32_t rd = 0, p = item_of_round(0); p < total && ok; p = item_of_round(++rd)) {
-            const DecItem it = dec_item<RNG>(pre, ri, p, a, tail_rows);
+            const DecItem it = dec_item(pre, ri, p, a.rows, tail_rows, a.num_rows, a.hkv);
             const int qb = ic & 1;
             if (cset == 0) {
                 if (!(ok = mbar_wait_warp(qc_full(qb), (ic >> 1) & 1, abort_flag))) break;
@@ -663,8 +454,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 const int vs = g % kVS;
                 const int nvalid = min(kKeys, it.hi - it.lo - j * kKeys);
                 if (!(ok = mbar_wait_warp(vc_full(vs), (g / kVS) & 1, abort_flag))) break;
-                widen_tile(smem + C::kV + vs * C::kTileBytes, nvalid, ct,
-                           [&](int r) { return !RNG || it.live(it.lo + j * kKeys + r); });
+                widen_tile(smem + C::kV + vs * C::kTileBytes, nvalid, ct, [](int) { return true; });
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_full(vs));
@@ -687,7 +477,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         bool ok = true;     // every wait of this thread so far completed
         bool stop = false;  // the joint decision to stop (FP8: the warpgroup's; bf16: both's), once per item
         for (int32_t rd = 0, p = item_of_round(0); p < total && !stop; p = item_of_round(++rd), ++ic) {
-            const DecItem it = dec_item<RNG>(pre, ri, p, a, tail_rows);
+            const DecItem it = dec_item(pre, ri, p, a.rows, tail_rows, a.num_rows, a.hkv);
             const float kd = F8 ? __ldg(a.k_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
             const float sl2 = a.scale * kd * kLog2e;
             // FP8: the power of two that undoes each head's q scaling (see q_to_e4m3_terms)
@@ -734,7 +524,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 const uint32_t g = gt + j;
                 if ((int)(g & 1) != wg) continue;
                 const int nvalid = min(kKeys, it.hi - it.lo - j * kKeys);
-                const bool valid = t < nvalid && (!RNG || it.live(it.lo + j * kKeys + t));
+                const bool valid = t < nvalid;
                 ok &= mbar_wait_warp(s_full(g & 1), (g >> 1) & 1, abort_flag);
                 tc_fence_after();
                 uint32_t s[kNS];
@@ -774,9 +564,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                     *reinterpret_cast<uint16_t*>(pcol + h * 128 + ((chunk ^ (h & 7)) << 4)) = hi;
                     *reinterpret_cast<uint16_t*>(pcol + (kGS + h) * 128 + ((chunk ^ (h & 7)) << 4)) = lo;
                 }
-                // RNG: also where the tile holds slots between the sinks and the window
-                const bool gaps = RNG && it.lo + j * kKeys < it.gap_end && it.gap_end > it.sinks;
-                if (!F8 && (nvalid < kKeys || gaps)) {
+                if (!F8 && nvalid < kKeys) {
                     // keys past the split's end: zero their V rows (unwritten cache slots in
                     // the last page, stale rows after it) once the tile has landed
                     const uint32_t vs = g % kVS;
@@ -844,14 +632,6 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                         const float f0 = fast_exp2(m_run[h] - M), f1 = fast_exp2(m1 - M);
                         const float L = L0 * f0 + L1 * f1;
                         const float O = acc[h] * f0 + xchg[kGS + h * kKeys + t] * f1;
-                        if (RNG && a.direct) {  // every row is one split: the result itself
-                            const size_t o = ((size_t)it.q_start * a.hq + it.hk * G + h) * kD + t;
-                            reinterpret_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
-                            if (t == 0)
-                                a.lse[(size_t)(it.hk * G + h) * a.total_q + it.q_start] =
-                                    L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
-                            continue;
-                        }
                         const size_t slot = ((size_t)it.ri * a.hq + it.hk * G + h) * (2 * max_splits) + it.split;
                         dec_out[slot * kD + t] = L > 0.f ? O / L : 0.f;
                         if (t == 0) dec_lse[slot] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
@@ -873,7 +653,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
     }
 }
 
-template <bool F8, int GP, bool RNG>
+template <bool F8, int GP>
 int launch_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, cudaStream_t stream,
               int grid) {
     const int64_t slots = a.num_blocks * a.block_size;
@@ -889,17 +669,12 @@ int launch_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_
     if (!maps) return PCP_ERR_CUDA;
     const int smem = TcCfg<F8, GP>::kSmem;
     cudaError_t e =
-        cudaFuncSetAttribute(decode_tc_kernel<F8, GP, RNG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(decode_tc_kernel<F8, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     const int ctas = grid > 0 && grid < num_sms() ? grid : num_sms();
-    if (RNG) {
-        e = launch_chained(decode_tc_kernel<F8, GP, RNG>, dim3(ctas), dim3(tc_threads(F8, GP)), smem, stream, tq, tk, tv,
-                           a, dec_out, dec_lse, max_splits, q_rows);
-    } else {
-        decode_tc_kernel<F8, GP, RNG><<<ctas, tc_threads(F8, GP), smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
-                                                                                  max_splits, q_rows);
-        e = cudaGetLastError();
-    }
+    decode_tc_kernel<F8, GP><<<ctas, tc_threads(F8, GP), smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
+                                                                              max_splits, q_rows);
+    e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }
@@ -912,34 +687,23 @@ bool decode_tc_applies(const PrefillArgs& a) {
            a.block_size <= kKeys && kKeys % a.block_size == 0;
 }
 
-namespace {
-
-template <bool RNG>
-int launch_tc_any(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits, cudaStream_t stream,
-                  int grid) {
+int launch_decode_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
+                     cudaStream_t stream, int grid) {
     if (!decode_tc_applies(a)) return PCP_ERR_UNSUPPORTED;
     const int G = a.hq / a.hkv;
     // heads per group padded to a power of two (the padded heads' results are not written)
     const int GP = G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : G <= 8 ? 8 : 16;
     if (a.k_descale) {
-        if (GP == 1) return launch_tc<true, 1, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
-        if (GP == 2) return launch_tc<true, 2, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
-        if (GP == 4) return launch_tc<true, 4, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
-        return launch_tc<true, 8, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
+        if (GP == 1) return launch_tc<true, 1>(a, dec_out, dec_lse, max_splits, stream, grid);
+        if (GP == 2) return launch_tc<true, 2>(a, dec_out, dec_lse, max_splits, stream, grid);
+        if (GP == 4) return launch_tc<true, 4>(a, dec_out, dec_lse, max_splits, stream, grid);
+        return launch_tc<true, 8>(a, dec_out, dec_lse, max_splits, stream, grid);
     }
-    if (GP == 1) return launch_tc<false, 1, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
-    if (GP == 2) return launch_tc<false, 2, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
-    if (GP == 4) return launch_tc<false, 4, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
-    if (GP == 8) return launch_tc<false, 8, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
-    return launch_tc<false, 16, RNG>(a, dec_out, dec_lse, max_splits, stream, grid);
-}
-
-}  // namespace
-
-int launch_decode_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
-                     cudaStream_t stream, int grid) {
-    return a.chunk > 0 ? launch_tc_any<true>(a, dec_out, dec_lse, max_splits, stream, grid)
-                       : launch_tc_any<false>(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (GP == 1) return launch_tc<false, 1>(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (GP == 2) return launch_tc<false, 2>(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (GP == 4) return launch_tc<false, 4>(a, dec_out, dec_lse, max_splits, stream, grid);
+    if (GP == 8) return launch_tc<false, 8>(a, dec_out, dec_lse, max_splits, stream, grid);
+    return launch_tc<false, 16>(a, dec_out, dec_lse, max_splits, stream, grid);
 }
 
 }  // namespace pcp

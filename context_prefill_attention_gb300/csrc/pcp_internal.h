@@ -230,20 +230,20 @@ int launch_decode_tc(const PrefillArgs& a, float* dec_out, float* dec_lse, int32
 // True when launch_decode takes the tensor-core kernel for these arguments (the
 // persistent kernel that PCP_ATTN_DECODE_SMS confines to a few SMs).
 bool decode_side_applies(const PrefillArgs& a);
-// Partials per split of the decode rows: two where the tensor-core kernel writes one
-// per softmax warpgroup.
-int decode_parts(const PrefillArgs& a);
 int launch_separate_merge(const PrefillArgs& a, cudaStream_t stream);
 // Window and shared-prefix calls: the schedule, the packed kernel over its work
-// list, the decode partials (decode_parts per split) and their merge.
+// list, the decode partials (one per split of chunk keys, max_splits slots per row and
+// q head; by launch_decode_pair where decode_tc_applies) and their merge.
 int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header,
                           int32_t* row_ok, int32_t* row_lo, MergeTask* merge, DecUnit* dec_units, int64_t max_units,
                           cudaStream_t stream);
 int launch_packed(const PrefillArgs& a, cudaStream_t stream);
 int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                         cudaStream_t stream);
+int launch_decode_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
+                       cudaStream_t stream);
 int launch_range_merge(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out, const float* dec_lse,
-                       int32_t max_splits, int parts, cudaStream_t stream);
+                       int32_t max_splits, cudaStream_t stream);
 int launch_cache_write(const void* k, const void* v, const int64_t* slot, int32_t num_tokens,
                        int32_t vec_per_tok, void* key_cache, void* value_cache, int64_t num_slots,
                        int32_t* status, cudaStream_t stream);

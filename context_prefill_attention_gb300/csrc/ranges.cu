@@ -27,8 +27,9 @@ struct RangeLayout {
 
 // Keys per decode split (a multiple of 128, at most kDecodeChunk): the length with
 // the shortest modelled time for rows of max_len slots. An SM takes its share of
-// the items one after the other; an item costs about 2.5 tiles of start-up on
-// top of its 128-key tiles, and every split one more partial to merge.
+// the items two at a time; a pair takes about 3 us to start and end, and a tile
+// of each 1.5 us by latency, 2.9 us once every SM draws on HBM; every split
+// is one more partial to merge.
 int32_t decode_chunk(int32_t num_rows, int32_t hkv, int64_t max_len) {
     const int64_t items = (int64_t)num_rows * hkv;
     double best = 0;
@@ -36,7 +37,9 @@ int32_t decode_chunk(int32_t num_rows, int32_t hkv, int64_t max_len) {
     for (int32_t c = kDecodeChunk; c >= kBlockN; c -= kBlockN) {
         const int64_t splits = (max_len + c - 1) / c;
         const int64_t tiles = ((max_len < c ? max_len : c) + kBlockN - 1) / kBlockN;
-        const double t = (double)((items * splits + kSms - 1) / kSms) * (2.5 + (double)tiles) + 0.3 * (double)splits;
+        const double pairs = (double)(items * splits) / (2 * kSms);
+        const double tile_us = 1.5 + 1.4 * (pairs < 1 ? pairs : 1);
+        const double t = (double)(int64_t)(pairs + 0.9999) * (3 + (double)tiles * tile_us) + 0.3 * (double)splits;
         if (c == kDecodeChunk || t < best) {
             best = t;
             best_chunk = c;
@@ -85,7 +88,7 @@ RangeLayout range_layout(int32_t num_rows, int32_t num_prefixes, int32_t total_q
     w.units_sorted = take((size_t)w.max_units * sizeof(PackedUnit));
     w.part_out = take((size_t)w.nparts * total_q * hq * d * 4);
     w.part_lse = take((size_t)w.nparts * total_q * hq * 4);
-    const size_t dec = (size_t)num_rows * hq * 2 * w.max_splits;
+    const size_t dec = (size_t)num_rows * hq * w.max_splits;
     w.dec_out = take(dec * d * 4);
     w.dec_lse = take(dec * 4);
     w.total = o;
@@ -193,10 +196,9 @@ int range_call(const RangeCall& c) {
     a.prefixes = c.prefixes;
     a.num_prefixes = shared ? c.num_prefixes : 0;
 
-    const int parts = decode_parts(a);
     a.num_sms = num_sms();
-    a.overlap = decode_side_applies(a);
-    a.direct = !shared && w.max_splits == 1 && parts == 1;
+    a.overlap = decode_tc_applies(a);
+    a.direct = !shared && w.max_splits == 1;
     MergeTask* tasks = reinterpret_cast<MergeTask*>(ws + w.merge);
     int rc = launch_range_schedule(a, reinterpret_cast<PackedUnit*>(ws + w.units),
                                    reinterpret_cast<PackedUnit*>(ws + w.units_sorted), ints(w.header), ints(w.row_ok),
@@ -214,7 +216,7 @@ int range_call(const RangeCall& c) {
         if (rc != PCP_OK) return rc;
     }
     if (a.direct) return PCP_OK;
-    return launch_range_merge(a, tasks, dec_out, dec_lse, w.max_splits, parts, c.stream);
+    return launch_range_merge(a, tasks, dec_out, dec_lse, w.max_splits, c.stream);
 }
 
 bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
