@@ -586,6 +586,31 @@ def pcp_kv_pages_workspace_size(num_blocks: int) -> int:
     return int(load().pcp_kv_pages_workspace_size(num_blocks))
 
 
+def _have(t, dtype, device: int, shape) -> bool:
+    """Whether ``t`` is a contiguous CUDA tensor of that type, device and shape."""
+    return type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device and device >= 0 \
+        and t.shape == shape and t.is_contiguous()
+
+
+def _i32_in(t, name: str, shape, like) -> None:
+    """``t`` checked as an int32 input of ``shape`` on the device of ``like``."""
+    if not _have(t, torch.int32, like.get_device(), shape):
+        _dev(t, name, I32, shape=shape, device=like.device)
+
+
+def _i32_out(t, name: str, shape, like):
+    """``t`` checked as an int32 output of ``shape`` on the device of ``like``, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=like.device)
+    _i32_in(t, name, shape, like)
+    return t
+
+
+def _status_in(status, like) -> None:
+    if status is not None and not (_have(status, torch.int32, like.get_device(), (1,))):
+        _status(status, like.device)
+
+
 def _check_pages(key_cache, value_cache, block_table, ref_count, status):
     dtype = key_cache.dtype if isinstance(key_cache, torch.Tensor) else None
     dev = key_cache.get_device() if dtype is not None else -1
@@ -599,32 +624,17 @@ def _check_pages(key_cache, value_cache, block_table, ref_count, status):
         _dev(value_cache, "value_cache", (dtype,), shape=tuple(key_cache.shape), device=device)
         _dev(block_table, "block_table", I32, shape=(-1, -1), device=device)
         _dev(ref_count, "ref_count", I32, shape=(int(key_cache.shape[0]),), device=device)
-    if status is not None:
-        _status(status, key_cache.device)
+    _status_in(status, key_cache)
     nb, bs, hkv, d = key_cache.shape
     return dev, nb, bs, hkv * d * key_cache.element_size()
 
 
-def _given(t, name: str):
-    if t is None:
-        raise TypeError(f"{name}: expected a torch.Tensor, got NoneType")
-    return t
-
-
-def _i32_buffer(t, name: str, shape, device):
-    """``t`` checked as an int32 buffer of ``shape``, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=device)
-    if type(t) is torch.Tensor and t.dtype is torch.int32 and t.is_cuda and t.shape == shape and t.is_contiguous() \
-            and t.device == device:
-        return t
-    return _dev(t, name, I32, shape=shape, device=device)
-
-
-def _pages_workspace(workspace, nb: int, device):
+def _pages_workspace(workspace, nb: int, like):
     if workspace is None:
-        return torch.empty(max(pcp_kv_pages_workspace_size(nb), 256), dtype=torch.uint8, device=device)
-    return _dev(workspace, "workspace", device=device)
+        return torch.empty(max(pcp_kv_pages_workspace_size(nb), 256), dtype=torch.uint8, device=like.device)
+    if not _ready(like.get_device(), (workspace, torch.uint8)):
+        _dev(workspace, "workspace", device=like.device)
+    return workspace
 
 
 def pcp_kv_fork(key_cache: torch.Tensor, value_cache: torch.Tensor, block_table: torch.Tensor, kv_len: torch.Tensor,
@@ -638,13 +648,13 @@ def pcp_kv_fork(key_cache: torch.Tensor, value_cache: torch.Tensor, block_table:
     [num_children, max_blocks], ref_count_out)``."""
     lib = load()
     dev, nb, bs, slot_bytes = _check_pages(key_cache, value_cache, block_table, ref_count, status)
-    device = key_cache.device
     R, mb = block_table.shape
-    _i32_buffer(_given(kv_len, "kv_len"), "kv_len", (R,), device)
-    N = _dev(parent, "parent", I32, shape=(-1,), device=device).shape[0]
-    block_table_out = _i32_buffer(block_table_out, "block_table_out", (N, mb), device)
-    ref_count_out = _i32_buffer(ref_count_out, "ref_count_out", (nb,), device)
-    workspace = _pages_workspace(workspace, nb, device)
+    _i32_in(kv_len, "kv_len", (R,), block_table)
+    N = parent.numel() if isinstance(parent, torch.Tensor) else 0
+    _i32_in(parent, "parent", (N,), block_table)
+    block_table_out = _i32_out(block_table_out, "block_table_out", (N, mb), block_table)
+    ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
+    workspace = _pages_workspace(workspace, nb, block_table)
     rc = _launch(lib.pcp_kv_fork, dev, stream, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, slot_bytes,
                  block_table.data_ptr(), R, mb, kv_len.data_ptr(), parent.data_ptr(), N, ref_count.data_ptr(),
                  block_table_out.data_ptr(), ref_count_out.data_ptr(), workspace.data_ptr(),
@@ -662,17 +672,18 @@ def pcp_kv_release(block_table: torch.Tensor, first_page: torch.Tensor, last_pag
     Returns ``(block_table_out, ref_count_out)``; pass the inputs themselves to
     work in place."""
     lib = load()
-    _dev(block_table, "block_table", I32, shape=(-1, -1))
-    device = block_table.device
+    dev = block_table.get_device() if isinstance(block_table, torch.Tensor) else -1
+    if dev < 0 or block_table.dim() != 2 or not _ready(dev, (block_table, torch.int32)):
+        _dev(block_table, "block_table", I32, shape=(-1, -1))
     R, mb = block_table.shape
-    _i32_buffer(_given(first_page, "first_page"), "first_page", (R,), device)
-    _i32_buffer(_given(last_page, "last_page"), "last_page", (R,), device)
-    nb = _dev(ref_count, "ref_count", I32, shape=(-1,), device=device).shape[0]
-    if status is not None:
-        _status(status, device)
-    block_table_out = _i32_buffer(block_table_out, "block_table_out", (R, mb), device)
-    ref_count_out = _i32_buffer(ref_count_out, "ref_count_out", (nb,), device)
-    rc = _launch(lib.pcp_kv_release, block_table.get_device(), stream, block_table.data_ptr(), R, mb,
+    _i32_in(first_page, "first_page", (R,), block_table)
+    _i32_in(last_page, "last_page", (R,), block_table)
+    nb = ref_count.numel() if isinstance(ref_count, torch.Tensor) else 0
+    _i32_in(ref_count, "ref_count", (nb,), block_table)
+    _status_in(status, block_table)
+    block_table_out = _i32_out(block_table_out, "block_table_out", (R, mb), block_table)
+    ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
+    rc = _launch(lib.pcp_kv_release, dev, stream, block_table.data_ptr(), R, mb,
                  first_page.data_ptr(), last_page.data_ptr(), ref_count.data_ptr(), nb, block_table_out.data_ptr(),
                  ref_count_out.data_ptr(), None if status is None else status.data_ptr())
     if rc:
@@ -689,12 +700,11 @@ def pcp_kv_compact(key_cache: torch.Tensor, value_cache: torch.Tensor, block_tab
     int32 ``[1]`` on the device."""
     lib = load()
     dev, nb, bs, slot_bytes = _check_pages(key_cache, value_cache, block_table, ref_count, status)
-    device = key_cache.device
     R, mb = block_table.shape
-    block_table_out = _i32_buffer(block_table_out, "block_table_out", (R, mb), device)
-    ref_count_out = _i32_buffer(ref_count_out, "ref_count_out", (nb,), device)
-    num_live = _i32_buffer(num_live, "num_live", (1,), device)
-    workspace = _pages_workspace(workspace, nb, device)
+    block_table_out = _i32_out(block_table_out, "block_table_out", (R, mb), block_table)
+    ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
+    num_live = _i32_out(num_live, "num_live", (1,), block_table)
+    workspace = _pages_workspace(workspace, nb, block_table)
     rc = _launch(lib.pcp_kv_compact, dev, stream, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, slot_bytes,
                  block_table.data_ptr(), R, mb, ref_count.data_ptr(), block_table_out.data_ptr(),
                  ref_count_out.data_ptr(), num_live.data_ptr(), workspace.data_ptr(),

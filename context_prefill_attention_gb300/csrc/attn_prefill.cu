@@ -1527,15 +1527,20 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         __syncthreads();  // off, lo_of and grp_of are rewritten
     }
     // The SMs of the decode rows and the prefixes' shards: lane n - 1 of warp 0 models n
-    // shards. SM times measured on GB300 (us): a decode item 1 and a 128-key tile 0.95
-    // (FP8 1.15) on a few SMs, a packed item 4.5 and a tile 1.75, a partial to merge
-    // total_q x hq x d x 8 bytes at 10 TB/s.
+    // shards. Times measured on GB300 (us): a decode item 1 and a 128-key tile 0.95
+    // (FP8 1.15) of an SM's time where few SMs draw on HBM, a tile (64 KB; FP8 32 KB)
+    // 1 / 95 (1 / 150) of the GPU's; a packed item 4.5 and a tile 1.75 (FP8 5.5, 1.95)
+    // of an SM's; a partial to merge total_q x hq x d x 8 bytes at 10 TB/s. Side by
+    // side, both kernels run about 6 % longer than alone.
     __syncthreads();
     if (warp == 0) {
-        const float dec_us = (float)a.hkv * (1.0f * cost[0] + (a.k_descale ? 1.15f : 0.95f) * cost[1]);
+        const bool f8 = a.k_descale != nullptr;
+        const float dec_us = (float)a.hkv * (1.0f * cost[0] + (f8 ? 1.15f : 0.95f) * cost[1]);
+        const float dec_all = 6.f + (float)a.hkv * cost[1] / (f8 ? 150.f : 95.f);
+        const float item_us = f8 ? 5.5f : 4.5f, tile_us = f8 ? 1.95f : 1.75f;
         const float merge_us = (float)a.total_q * a.hq * a.d * 8e-7f;
         const int32_t nsm = a.num_sms, most = min(32, max(1, a.nparts - 1));
-        float items = (float)cost[2], tiles = (float)cost[3];
+        float items = 0.f, tiles = 0.f;  // of the prefixes, per kv head
         int32_t longest = 0;
         for (int32_t g = 0; g < ng; ++g) {
             if (shards_of[g] == 0) continue;
@@ -1546,14 +1551,24 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
             tiles += (float)tok * t;
             longest = max(longest, (t + n - 1) / n);
         }
-        const float pack_us = (float)a.hkv * (4.5f * items + 1.75f * tiles);
+        const float pre_us = (float)a.hkv * (item_us * items + tile_us * tiles);
+        const float pack_us = pre_us + (float)a.hkv * (item_us * cost[2] + tile_us * cost[3]);
+        // the packed kernel on m SMs: equal items in rounds, shorter ones in the gaps
+        auto packed_on = [&](float m) {
+            float us = fmaxf(pack_us / m, longest ? item_us + tile_us * longest : 0.f);
+            if (items > 0.f) us = fmaxf(us, ceilf(items * a.hkv / m) * pre_us / (a.hkv * items));
+            return us;
+        };
+        float us = (dec_us > 0.f ? dec_all : 0.f) + packed_on((float)nsm);
         int32_t k = 0;
-        if (a.overlap && dec_us > 0.f && pack_us > 0.f)
-            k = max(1, min(nsm - 1, (int32_t)(nsm * dec_us / (dec_us + pack_us) + 0.5f)));
-        const float m = (float)(nsm - k);
-        const float rounds = ceilf(items * a.hkv / m);
-        float us = fmaxf(items > 0.f ? rounds * pack_us / (a.hkv * items) : 0.f, 4.5f + 1.75f * longest);
-        if (k > 0) us = fmaxf(us, dec_us / k);
+        if (a.overlap && dec_us > 0.f && pack_us > 0.f) {
+            const int32_t beside = max(1, min(nsm - 1, (int32_t)(nsm * dec_us / (dec_us + pack_us) + 0.5f)));
+            const float t = 1.06f * fmaxf(dec_us / beside, packed_on((float)(nsm - beside))) + 6.f;
+            if (t < us) {
+                us = t;
+                k = beside;
+            }
+        }
         us += (lane + 1) * merge_us;
         if (lane >= most) us = INFINITY;
         float best = us;
