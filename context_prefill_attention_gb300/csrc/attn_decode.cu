@@ -113,6 +113,10 @@ __global__ void __launch_bounds__(kDecThreads)
     using C = DecCfg<D, GMAX, F8>;
     constexpr int VEC = D / 16;
     const int split = blockIdx.x, hk = blockIdx.y, ri = blockIdx.z;
+    if constexpr (RNG) {  // launched behind the scheduler
+        grid_wait();
+        grid_launch_dependents();
+    }
     if (!a.row_ok[ri]) return;
     const pcp_row_t row = a.rows[ri];
     if (RNG ? row.q_len != 1 : !row.is_decode) return;
@@ -475,7 +479,8 @@ __global__ void __launch_bounds__(256)
     const int32_t at = (int32_t)(job / a.hq), h = (int32_t)(job - (int64_t)at * a.hq);
     if (at >= (a.num_prefixes > 0 ? a.total_q : a.num_rows)) return;
     const int4 raw = *reinterpret_cast<const int4*>(tasks + at);
-    const MergeTask task{raw.x, raw.y, raw.z, min(raw.w, a.num_units[4])};
+    // (window calls have no prefixes, and a call without the scheduler no header)
+    const MergeTask task{raw.x, raw.y, raw.z, a.num_prefixes > 0 ? min(raw.w, a.num_units[4]) : 0};
     if (task.row < 0) return;
     const bool one = task.splits > 0;
     const int32_t t = one ? task.token : at;
@@ -543,9 +548,14 @@ int launch_decode_dgf(const PrefillArgs& a, float* dec_out, float* dec_lse, int3
         cudaFuncSetAttribute(decode_kernel<D, GMAX, F8, RNG>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     dim3 grid(max_splits, a.hkv, a.num_rows);
-    decode_kernel<D, GMAX, F8, RNG><<<grid, kDecThreads, smem, stream>>>(tk, tv, a, dec_out, dec_lse, max_splits,
-                                                                         box_rows);
-    e = cudaGetLastError();
+    if (RNG) {
+        e = launch_chained(decode_kernel<D, GMAX, F8, RNG>, grid, dim3(kDecThreads), smem, stream, tk, tv, a, dec_out,
+                           dec_lse, max_splits, box_rows);
+    } else {
+        decode_kernel<D, GMAX, F8, RNG><<<grid, kDecThreads, smem, stream>>>(tk, tv, a, dec_out, dec_lse, max_splits,
+                                                                             box_rows);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }

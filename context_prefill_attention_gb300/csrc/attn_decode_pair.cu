@@ -20,7 +20,10 @@
 //    warpgroup (one with 16 heads, for lack of shared memory);
 //  * the producers look one tile ahead: a tile's pages, and behind an item's last
 //    tile the next items' records, are read before the wait for the current stage.
-// Launched behind the scheduler (launch_chained), on header[2] of the SMs.
+// Launched behind the scheduler (launch_chained), on header[2] of the SMs. A call of
+// a few one-token rows whose items all fit the SMs at once (a.inline_items) has no
+// scheduler: one warp of each CTA reads the rows (kInlineRows at most) and finds
+// the CTA's two items itself. Measured, 4 rows with a window of 1024: TODO us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -64,8 +67,9 @@ struct PairCfg {
     static constexpr int kQs = kSum + 2 * 2 * 4 * kGS * 4;
     static constexpr int kBar = kQs + 8 * kGS * 4;
     static constexpr int kNumBars = 2 * kKS + 3 * kVS + 3 * 2 * kQB + 8 + 4 * 2;
-    static constexpr int kMisc = kBar + kNumBars * 8;  // TMEM address, abort flag
-    static constexpr int kSmem = kMisc + 16 + 1024;    // + alignment slack
+    static constexpr int kMisc = kBar + kNumBars * 8;  // TMEM address, abort flag, item count
+    static constexpr int kOwn = kMisc + 16;            // PairItem [2]: a.inline_items
+    static constexpr int kSmem = kOwn + 2 * 40 + 1024;  // + alignment slack
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * kNS;
     static constexpr uint32_t kTmemCols = 2 * kNS + 2 * kNO <= 64 ? 64 : 128;
     static constexpr uint32_t kIdescS = F8 ? idesc_e4m3(128, kNS) : idesc_bf16(128, kN, false, false);
@@ -102,6 +106,78 @@ __device__ __forceinline__ PairItem pair_item(const PrefillArgs& a, int32_t p, i
     it.shift = y.w;
     it.nt = (it.hi - it.lo + kKeys - 1) / kKeys;
     return it;
+}
+
+static_assert(sizeof(PairItem) == 40, "two of them fit at PairCfg::kOwn");
+
+// a.inline_items: one warp's work of finding the items `p0` and `p1` (-1: none) among
+// all rows, splits and kv heads (row by row, split by split, head by head); returns
+// the item count. CTA 0 also reports bad rows and writes the merge records.
+constexpr int kInlineRows = 64;
+__device__ __forceinline__ int32_t inline_items(const PrefillArgs& a, int32_t p0, int32_t p1, PairItem* own,
+                                                int lane) {
+    constexpr int kPer = kInlineRows / 32;
+    const int64_t max_kv = (int64_t)a.max_blocks * a.block_size;
+    pcp_row_t row[kPer];
+    KeyRange kr[kPer];
+    int32_t splits[kPer], before[kPer], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int32_t ri = lane * kPer + k;
+        row[k] = ri < a.num_rows ? a.rows[ri] : pcp_row_t{};
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int32_t ri = lane * kPer + k;
+        const bool ok = ri < a.num_rows && row_in_range(row[k], a.num_reqs, a.total_q, max_kv) && row[k].q_len == 1;
+        if (!ok) row[k].kv_end = 0;
+        kr[k] = key_range(a, row[k], 0);
+        splits[k] = ok ? (kr[k].len + a.chunk - 1) / a.chunk : 0;
+        sum += splits[k];
+        if (blockIdx.x == 0 && ri < a.num_rows) {
+            if (!ok) report_status(a.status, PCP_ERR_RANGE);
+            a.merge[ri] = MergeTask{ok ? ri : -1, row[k].q_start, splits[k], 0};
+        }
+    }
+    int32_t at = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += x;
+    }
+    const int32_t total = __shfl_sync(0xffffffffu, at, 31) * a.hkv;
+    at -= sum;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        before[k] = at;
+        at += splits[k];
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int32_t p = w ? p1 : p0;
+        if (p < 0 || p >= total) {
+            if (lane == 0) own[w] = PairItem{};
+            continue;
+        }
+        const int32_t n = p / a.hkv;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (n >= before[k] && n < before[k] + splits[k]) {
+                PairItem it;
+                it.row = lane * kPer + k;
+                it.req = row[k].req;
+                it.q_start = row[k].q_start;
+                it.hk = p - n * a.hkv;
+                it.lo = (n - before[k]) * a.chunk;
+                it.hi = min(kr[k].len, it.lo + a.chunk);
+                it.nt = (it.hi - it.lo + kKeys - 1) / kKeys;
+                it.sinks = kr[k].sinks;
+                it.gap_end = kr[k].lo - kr[k].shift;
+                it.shift = kr[k].shift;
+                own[w] = it;
+            }
+    }
+    return total;
 }
 
 template <bool F8, int GP>
@@ -177,19 +253,34 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    // the scheduler's lists are read from here on
-    grid_wait();
-    grid_launch_dependents();
+    PairItem* own = reinterpret_cast<PairItem*>(smem + C::kOwn);
+    int32_t* own_total = reinterpret_cast<int32_t*>(smem + C::kMisc + 8);
+    if (a.inline_items) {
+        grid_launch_dependents();
+        if (warp == 0) {
+            const int32_t n = inline_items(a, (int32_t)blockIdx.x, 2 * a.num_sms - 1 - (int32_t)blockIdx.x, own, lane);
+            if (lane == 0) *own_total = n;
+        }
+        __syncthreads();
+    } else {
+        // the scheduler's lists are read from here on
+        grid_wait();
+        grid_launch_dependents();
+    }
     // CTAs that take items: as many as the scheduler gave the decode rows. Items in
     // snake order (forward on even rounds, backward on odd ones) over the list, longest
     // first; rounds 2q and 2q + 1 are pair q.
-    const int32_t step = a.num_units[2];
-    const int32_t total = (int32_t)blockIdx.x < step ? a.num_units[1] : 0;
+    const int32_t step = a.inline_items ? a.num_sms : a.num_units[2];
+    const int32_t total = a.inline_items ? *own_total : (int32_t)blockIdx.x < step ? a.num_units[1] : 0;
     // (A CTA without items gets `total` in every round: the snake's backward rounds
     // would be negative for it.)
     auto item_of_round = [&](int32_t rd) -> int32_t {
         if ((int32_t)blockIdx.x >= step) return total;
         return rd * step + ((rd & 1) ? step - 1 - (int32_t)blockIdx.x : (int32_t)blockIdx.x);
+    };
+    auto item_at = [&](int32_t rd) -> PairItem {
+        if (a.inline_items) return rd < 2 ? own[rd] : PairItem{};
+        return pair_item(a, item_of_round(rd), total);
     };
     tc_fence_before();
     __syncthreads();
@@ -211,7 +302,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         const uint32_t q_bytes = 2u * (uint32_t)q_rows * 128u;
         auto full_of = [&](int st) { return is_k ? k_full(st) : (F8 ? vc_full(st) : v_full(st)); };
         // cursor over the stream: tile j of item w of pair q
-        PairItem i0 = pair_item(a, item_of_round(0), total), i1 = pair_item(a, item_of_round(1), total);
+        PairItem i0 = item_at(0), i1 = item_at(1);
         int32_t q = 0, j = 0;
         int w = 0;
         auto cur = [&]() -> const PairItem& { return w ? i1 : i0; };
@@ -241,8 +332,8 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 ++j;
             } else {
                 ++q;
-                i0 = pair_item(a, item_of_round(2 * q), total);
-                i1 = pair_item(a, item_of_round(2 * q + 1), total);
+                i0 = item_at(2 * q);
+                i1 = item_at(2 * q + 1);
                 w = 0;
                 j = 0;
             }
@@ -314,8 +405,8 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
             bool ok = true;
             const bool s_role = warp == kMmaWarp;
             for (int32_t q = 0; ok && item_of_round(2 * q) < total; ++q) {
-                const int32_t nt[2] = {pair_item(a, item_of_round(2 * q), total).nt,
-                                       pair_item(a, item_of_round(2 * q + 1), total).nt};
+                const int32_t nt[2] = {item_at(2 * q).nt,
+                                       item_at(2 * q + 1).nt};
                 const int32_t most = max(nt[0], nt[1]);
                 for (int j = 0; j < most && ok; ++j) {
 #pragma unroll
@@ -381,8 +472,8 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         uint32_t g = 0;
         bool ok = true;
         for (int32_t q = 0; ok && item_of_round(2 * q) < total; ++q) {
-            const PairItem it[2] = {pair_item(a, item_of_round(2 * q), total),
-                                    pair_item(a, item_of_round(2 * q + 1), total)};
+            const PairItem it[2] = {item_at(2 * q),
+                                    item_at(2 * q + 1)};
             const int32_t most = max(it[0].nt, it[1].nt);
             for (int j = 0; j < most && ok; ++j) {
 #pragma unroll
@@ -436,8 +527,8 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         bool ok = true;     // every wait of this thread so far completed
         bool stop = false;  // the warpgroup's joint decision to stop, once per item
         for (int32_t q = 0; !stop && item_of_round(2 * q + wg) < total; ++q) {
-            const PairItem it = pair_item(a, item_of_round(2 * q + wg), total);
-            const int32_t n_other = pair_item(a, item_of_round(2 * q + 1 - wg), total).nt;
+            const PairItem it = item_at(2 * q + wg);
+            const int32_t n_other = item_at(2 * q + 1 - wg).nt;
             const float kd = F8 ? __ldg(a.k_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
             const float sl2 = a.scale * kd * kLog2e;
             // FP8: the power of two that undoes each head's q scaling (see q_to_e4m3_terms)
@@ -591,14 +682,26 @@ int launch_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t ma
     const int smem = PairCfg<F8, GP>::kSmem;
     cudaError_t e =
         cudaFuncSetAttribute(decode_pair_kernel<F8, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-        e = launch_chained(decode_pair_kernel<F8, GP>, dim3(a.num_sms), dim3(tc_threads(F8, GP)), smem, stream, tq, tk,
-                           tv, a, dec_out, dec_lse, max_splits, q_rows);
+    if (e == cudaSuccess) {
+        if (a.inline_items) {  // nothing of this call to be chained behind
+            decode_pair_kernel<F8, GP><<<a.num_sms, tc_threads(F8, GP), smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
+                                                                                      max_splits, q_rows);
+            e = cudaGetLastError();
+        } else {
+            e = launch_chained(decode_pair_kernel<F8, GP>, dim3(a.num_sms), dim3(tc_threads(F8, GP)), smem, stream, tq,
+                               tk, tv, a, dec_out, dec_lse, max_splits, q_rows);
+        }
+    }
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }
 
 }  // namespace
+
+bool decode_inline_applies(const PrefillArgs& a, int32_t max_splits) {
+    return decode_tc_applies(a) && a.num_prefixes == 0 && a.total_q <= a.num_rows && a.num_rows <= kInlineRows &&
+           (int64_t)a.num_rows * a.hkv * max_splits <= 2 * a.num_sms;
+}
 
 int launch_decode_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                        cudaStream_t stream) {

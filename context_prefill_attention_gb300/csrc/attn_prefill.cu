@@ -1127,6 +1127,7 @@ constexpr int kSchedThreads = 1024;
 constexpr int kSortCap = 4096;
 constexpr int kCostBuckets = 2 * kSortCap;  // int32 counters in the same 32 KB as the sort keys
 
+template <int NT = kSchedThreads>
 __device__ __forceinline__ int32_t block_exclusive_scan(int32_t v, int32_t* warp_sums, int32_t* total) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int32_t x = v;
@@ -1138,7 +1139,7 @@ __device__ __forceinline__ int32_t block_exclusive_scan(int32_t v, int32_t* warp
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int32_t w = lane < kSchedThreads / 32 ? warp_sums[lane] : 0;
+        int32_t w = lane < NT / 32 ? warp_sums[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int32_t y = __shfl_up_sync(0xffffffffu, w, o);
@@ -1148,17 +1149,9 @@ __device__ __forceinline__ int32_t block_exclusive_scan(int32_t v, int32_t* warp
     }
     __syncthreads();
     const int32_t before = (warp > 0 ? warp_sums[warp - 1] : 0) + x - v;
-    *total = warp_sums[kSchedThreads / 32 - 1];
+    *total = warp_sums[NT / 32 - 1];
     __syncthreads();
     return before;
-}
-
-// The checks every row of a plan has to pass.
-__device__ __forceinline__ bool row_in_range(const pcp_row_t& row, int32_t num_reqs, int32_t total_q, int64_t max_kv) {
-    return row.req >= 0 && row.req < num_reqs && row.q_len >= 1 && row.q_start >= 0 &&
-           (int64_t)row.q_start + row.q_len <= total_q && row.kv_end >= row.q_len && row.kv_end <= max_kv &&
-           row.ctx_len >= 0 && row.ctx_len <= row.kv_end &&
-           (row.is_decode == 0 || (row.is_decode == 1 && row.q_len == 1));
 }
 
 // Key tiles a unit's item walks (its cost in the schedule).
@@ -1178,10 +1171,11 @@ constexpr int kTailBuckets = kDecodeChunk / kBlockN;
 // so that the list, and with it every sum's order, is the same in every run.
 // Called by the whole block, once per kSchedThreads rows in row order; fill[]
 // (shared, zeroed) counts the rows placed so far, warp_cnt is scratch.
+template <int NT = kSchedThreads>
 __device__ __forceinline__ int32_t tail_place(int32_t b, const int32_t* off, int32_t* fill,
                                               int32_t (*warp_cnt)[kTailBuckets + 1]) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    for (int i = threadIdx.x; i < (kSchedThreads / 32) * (kTailBuckets + 1); i += kSchedThreads)
+    for (int i = threadIdx.x; i < (NT / 32) * (kTailBuckets + 1); i += NT)
         (&warp_cnt[0][0])[i] = 0;
     __syncthreads();
     const uint32_t same = __match_any_sync(0xffffffffu, b);
@@ -1189,7 +1183,7 @@ __device__ __forceinline__ int32_t tail_place(int32_t b, const int32_t* off, int
     __syncthreads();
     if (threadIdx.x <= kTailBuckets) {  // running counts over the warps
         int32_t n = fill[threadIdx.x];
-        for (int w = 0; w < kSchedThreads / 32; ++w) {
+        for (int w = 0; w < NT / 32; ++w) {
             const int32_t c = warp_cnt[w][threadIdx.x];
             warp_cnt[w][threadIdx.x] = n;
             n += c;
@@ -1385,29 +1379,32 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
 // fields in shared memory, its first unit in registers; units are dealt to the
 // threads by a search over the rows' running counts (a thread per row would
 // write a long row's units one by one) and ordered by one counting pass.
-constexpr int kMaxGroups = kSchedThreads;
-constexpr int kCostClasses = kSchedThreads;
+// NT threads, and as many rows a round, groups and cost classes: kSchedThreads, or
+// kSchedSmall where rows and groups are few (a barrier of fewer warps costs less).
+constexpr int kSchedSmall = 256;
 
-// Index of the last entry of off[0, kSchedThreads) that is at most u (off ascending from 0).
+// Index of the last entry of off[0, NT) that is at most u (off ascending from 0).
+template <int NT>
 __device__ __forceinline__ int32_t last_at_most(const int32_t* off, int32_t u) {
     int32_t at = 0;
 #pragma unroll
-    for (int step = kSchedThreads / 2; step > 0; step /= 2)
+    for (int step = NT / 2; step > 0; step /= 2)
         if (off[at + step] <= u) at += step;
     return at;
 }
 
-__global__ void __launch_bounds__(kSchedThreads, 1)
+template <int NT>
+__global__ void __launch_bounds__(NT, 1)
     range_schedule_kernel(PrefillArgs a, PackedUnit* units, PackedUnit* sorted, int32_t* header, int32_t* row_ok,
                           int32_t* row_lo, MergeTask* merge, DecUnit* dec_units, int64_t max_units) {
     __shared__ int32_t warp_sums[32];
     __shared__ int32_t tail_cnt[kTailBuckets + 1], tail_off[kTailBuckets + 1], tail_fill[kTailBuckets + 1];
-    __shared__ int32_t tail_warp[kSchedThreads / 32][kTailBuckets + 1];
-    __shared__ __align__(16) pcp_prefix_t prefix[kMaxGroups];
-    __shared__ int32_t shards_of[kMaxGroups];    // 0: a bad group
-    __shared__ int32_t off[kSchedThreads];       // first unit of each row (group) of the round
-    __shared__ int32_t lo_of[kSchedThreads], grp_of[kSchedThreads];
-    __shared__ int32_t classes[kCostClasses];    // units per cost class, then the class's next place
+    __shared__ int32_t tail_warp[NT / 32][kTailBuckets + 1];
+    __shared__ __align__(16) pcp_prefix_t prefix[NT];
+    __shared__ int32_t shards_of[NT];    // 0: a bad group
+    __shared__ int32_t off[NT];       // first unit of each row (group) of the round
+    __shared__ int32_t lo_of[NT], grp_of[NT];
+    __shared__ int32_t classes[NT];    // units per cost class, then the class's next place
     __shared__ int32_t cost[4];  // decode splits and tiles, packed units and tiles (per kv head)
     __shared__ int32_t max_shards;
     grid_launch_dependents();  // the decode kernel sets itself up meanwhile
@@ -1426,7 +1423,7 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
     classes[tid] = 0;
     if (tid < ng) prefix[tid] = a.prefixes[tid];
     if (ng > 0)
-        for (int32_t t = tid; t < a.total_q; t += kSchedThreads) merge[t] = MergeTask{-1, 0, 0, 0};
+        for (int32_t t = tid; t < a.total_q; t += NT) merge[t] = MergeTask{-1, 0, 0, 0};
     __syncthreads();
     // groups: fields in range, and the tokens after those of every earlier group
     if (tid < ng) {
@@ -1439,18 +1436,18 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
     }
     if (ng > 0) __syncthreads();
     auto class_of = [](const PackedUnit& u) {
-        return kCostClasses - 1 - min((u.k_end + kBlockN - 1) / kBlockN, kCostClasses - 1);
+        return NT - 1 - min((u.k_end + kBlockN - 1) / kBlockN, NT - 1);
     };
     PackedUnit mine{};  // unit tid, if there is one
-    // unit i of the list, by the thread of i's place in its round of kSchedThreads
+    // unit i of the list, by the thread of i's place in its round of NT
     auto put = [&](int32_t i, const PackedUnit& x) {
-        if (i < kSchedThreads) mine = x;
+        if (i < NT) mine = x;
         else units[i] = x;
         atomicAdd(&classes[class_of(x)], 1);
     };
     int32_t base = 0;          // packed units so far
     int32_t my_lo = 0, my_len = 0, my_splits = 0;  // the first round's row, as a decode row (0 splits: none)
-    for (int32_t r0 = 0; r0 < num_rows; r0 += kSchedThreads) {
+    for (int32_t r0 = 0; r0 < num_rows; r0 += NT) {
         const int32_t ri = r0 + tid;
         if (r0 > 0 && ri < num_rows) row = a.rows[ri];
         int32_t cnt = 0, splits = 0, dec_tiles = 0, lo = 0, grp = -1;
@@ -1501,11 +1498,11 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         grp_of[tid] = grp;
         if (a.total_q <= num_rows && ng == 0) continue;  // no row is longer than one token
         int32_t tot;
-        off[tid] = block_exclusive_scan(cnt, warp_sums, &tot);
+        off[tid] = block_exclusive_scan<NT>(cnt, warp_sums, &tot);
         __syncthreads();
         int32_t tiles = 0;
-        for (int32_t i = base + (tid - base & (kSchedThreads - 1)); i < base + tot && i < max_units; i += kSchedThreads) {
-            const int32_t at = last_at_most(off, i - base);
+        for (int32_t i = base + (tid - base & (NT - 1)); i < base + tot && i < max_units; i += NT) {
+            const int32_t at = last_at_most<NT>(off, i - base);
             const pcp_row_t r = a.rows[r0 + at];
             const PackedUnit x = packed_unit(a, r.req, r.q_start, r.q_len, r.kv_end - r.q_len, i - base - off[at], span,
                                              lo_of[at], r.kv_end, grp_of[at] >= 0 ? a.nparts : 0);
@@ -1515,8 +1512,8 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         if (tiles) atomicAdd(&cost[3], tiles);
         if (tid == 0) cost[2] += tot;
         if (ng > 0)  // a warp per unit
-            for (int32_t u = warp; u < tot; u += kSchedThreads / 32) {
-                const int32_t at = last_at_most(off, u);
+            for (int32_t u = warp; u < tot; u += NT / 32) {
+                const int32_t at = last_at_most<NT>(off, u);
                 if (grp_of[at] < 0) continue;
                 const pcp_row_t r = a.rows[r0 + at];
                 const int32_t t1 = min(r.q_len, (u - off[at] + 1) * span);
@@ -1597,15 +1594,16 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         int32_t cnt = 0;
         if (tid < ng) cnt = min(shards_of[tid], max_shards) * ((prefix[tid].q_len + span - 1) / span);
         int32_t tot;
-        off[tid] = block_exclusive_scan(cnt, warp_sums, &tot);
+        off[tid] = block_exclusive_scan<NT>(cnt, warp_sums, &tot);
         __syncthreads();
-        for (int32_t i = base + (tid - base & (kSchedThreads - 1)); i < base + tot && i < max_units; i += kSchedThreads) {
-            const int32_t at = last_at_most(off, i - base), u = i - base - off[at];
+        for (int32_t i = base + (tid - base & (NT - 1)); i < base + tot && i < max_units; i += NT) {
+            const int32_t at = last_at_most<NT>(off, i - base), u = i - base - off[at];
             const pcp_prefix_t p = prefix[at];
             const int32_t shards = min(shards_of[at], max_shards), pages = (p.prefix_len + bs - 1) / bs;
             const int32_t sh = u % shards, mt = u / shards;
-            const int32_t k_lo = (int32_t)((int64_t)pages * sh / shards) * bs;
-            const int32_t k_hi = (int32_t)min((int64_t)p.prefix_len, (int64_t)pages * (sh + 1) / shards * bs);
+            // floor(pages x sh / shards) in 32 bits
+            auto cut = [&](int32_t n) { return pages / shards * n + pages % shards * n / shards; };
+            const int32_t k_lo = cut(sh) * bs, k_hi = (int32_t)min((int64_t)p.prefix_len, (int64_t)cut(sh + 1) * bs);
             PackedUnit x = packed_unit(a, p.req, p.q_start, p.q_len, 0, mt, span, k_lo, k_hi, 1 + sh);
             x.pos0 = k_hi;  // every query lies past the prefix
             x.k_lo = k_lo;
@@ -1622,11 +1620,11 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
         // longest first (units of one class in any order: an item writes only its own
         // results, which do not depend on its place)
         int32_t tot;
-        const int32_t first = block_exclusive_scan(classes[tid], warp_sums, &tot);
+        const int32_t first = block_exclusive_scan<NT>(classes[tid], warp_sums, &tot);
         classes[tid] = first;
         __syncthreads();
-        for (int32_t i = tid; i < n; i += kSchedThreads) {
-            const PackedUnit x = i < kSchedThreads ? mine : units[i];
+        for (int32_t i = tid; i < n; i += NT) {
+            const PackedUnit x = i < NT ? mine : units[i];
             sorted[atomicAdd(&classes[class_of(x)], 1)] = x;
         }
         __syncthreads();  // off is rewritten
@@ -1634,7 +1632,7 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
     if (cost[0] == 0 || num_rows > kDecTcMaxRows) return;
     // the decode splits, by a search over the rows' running counts
     int32_t tot;
-    const int32_t first = block_exclusive_scan(my_splits, warp_sums, &tot);
+    const int32_t first = block_exclusive_scan<NT>(my_splits, warp_sums, &tot);
     off[tid] = first;
     // the rows' fields, in the shared memory of the counting pass and the groups
     int32_t* len_of = classes;
@@ -1643,12 +1641,12 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
     len_of[tid] = my_len;
     row_of[tid] = make_int4(row.req, row.q_start, my_lo, row.kv_end);
     __syncthreads();
-    for (int32_t i0 = 0; i0 < tot; i0 += kSchedThreads) {
+    for (int32_t i0 = 0; i0 < tot; i0 += NT) {
         const int32_t i = i0 + tid;
         DecUnit x{};
         int32_t b = 0;
         if (i < tot) {
-            const int32_t at = last_at_most(off, i);
+            const int32_t at = last_at_most<NT>(off, i);
             const int4 fields = row_of[at];
             pcp_row_t r{};
             r.kv_end = fields.w;
@@ -1663,7 +1661,7 @@ __global__ void __launch_bounds__(kSchedThreads, 1)
             x.shift = kr.shift;
             b = (x.hi - x.lo + kBlockN - 1) / kBlockN;
         }
-        const int32_t to = tail_place(b, tail_off, tail_fill, tail_warp);
+        const int32_t to = tail_place<NT>(b, tail_off, tail_fill, tail_warp);
         if (b) dec_units[to] = x;
     }
 }
@@ -1770,8 +1768,12 @@ int launch_schedule(const PrefillArgs& a, int32_t flags, Unit* units, Unit* unit
 int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* units_sorted, int32_t* header,
                           int32_t* row_ok, int32_t* row_lo, MergeTask* merge, DecUnit* dec_units, int64_t max_units,
                           cudaStream_t stream) {
-    range_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(a, units, units_sorted, header, row_ok, row_lo, merge,
-                                                           dec_units, max_units);
+    if (a.num_rows <= kSchedSmall && a.num_prefixes <= kSchedSmall && a.total_q <= 8 * kSchedSmall)
+        range_schedule_kernel<kSchedSmall><<<1, kSchedSmall, 0, stream>>>(a, units, units_sorted, header, row_ok, row_lo,
+                                                                          merge, dec_units, max_units);
+    else
+        range_schedule_kernel<kSchedThreads><<<1, kSchedThreads, 0, stream>>>(a, units, units_sorted, header, row_ok,
+                                                                              row_lo, merge, dec_units, max_units);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;

@@ -133,6 +133,8 @@ struct PrefillArgs {
     int32_t window, sinks;      // keys a query sees: the last `window` ones and the first `sinks`
     int32_t num_sms;            // CTAs of the persistent kernels
     int32_t overlap;            // the decode kernel is the persistent one: it can share the SMs
+    int32_t inline_items;       // the decode kernel finds its items itself (decode_inline_applies)
+    MergeTask* merge;           // ... and writes the merge records
     int32_t direct;             // decode rows have one partial each: written straight to out and lse
     int32_t slots;              // token tiles per packed item: 1 or 2
     const DecUnit* dec_units;   // the decode list, longest first
@@ -171,6 +173,14 @@ struct KeyRange {
     int32_t lo, sinks, sink_slots, shift, len;
     __device__ __forceinline__ bool live(int32_t v) const { return v < sinks || v >= lo - shift; }
 };
+
+// The checks every row of a plan has to pass.
+__device__ __forceinline__ bool row_in_range(const pcp_row_t& row, int32_t num_reqs, int32_t total_q, int64_t max_kv) {
+    return row.req >= 0 && row.req < num_reqs && row.q_len >= 1 && row.q_start >= 0 &&
+           (int64_t)row.q_start + row.q_len <= total_q && row.kv_end >= row.q_len && row.kv_end <= max_kv &&
+           row.ctx_len >= 0 && row.ctx_len <= row.kv_end &&
+           (row.is_decode == 0 || (row.is_decode == 1 && row.q_len == 1));
+}
 
 __device__ __forceinline__ KeyRange key_range(const PrefillArgs& a, const pcp_row_t& row, int32_t row_lo) {
     KeyRange k;
@@ -240,6 +250,9 @@ int launch_range_schedule(const PrefillArgs& a, PackedUnit* units, PackedUnit* u
 int launch_packed(const PrefillArgs& a, cudaStream_t stream);
 int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                         cudaStream_t stream);
+// Whether a window call's rows are one-token rows (as many as tokens) few enough for
+// the decode kernel to find its items without the scheduler.
+bool decode_inline_applies(const PrefillArgs& a, int32_t max_splits);
 int launch_decode_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                        cudaStream_t stream);
 int launch_range_merge(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out, const float* dec_lse,

@@ -200,7 +200,11 @@ int range_call(const RangeCall& c) {
     a.overlap = decode_tc_applies(a);
     a.direct = !shared && w.max_splits == 1;
     MergeTask* tasks = reinterpret_cast<MergeTask*>(ws + w.merge);
-    int rc = launch_range_schedule(a, reinterpret_cast<PackedUnit*>(ws + w.units),
+    a.merge = tasks;
+    a.inline_items = decode_inline_applies(a, w.max_splits);
+    int rc = PCP_OK;
+    if (!a.inline_items)
+        rc = launch_range_schedule(a, reinterpret_cast<PackedUnit*>(ws + w.units),
                                    reinterpret_cast<PackedUnit*>(ws + w.units_sorted), ints(w.header), ints(w.row_ok),
                                    ints(w.row_lo), tasks, reinterpret_cast<DecUnit*>(ws + w.dec_units), w.max_units,
                                    c.stream);
