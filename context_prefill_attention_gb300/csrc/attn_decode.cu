@@ -462,12 +462,12 @@ __global__ void __launch_bounds__(256)
 // a group also those of the prefix's shards (partials 0 .. shards - 1). A longer
 // row outside every group was written by the packed kernel.
 //
-// Bound by the partials' bytes once many warps are in flight: a warp per (token,
-// head), lane l with D / 32 dims; all it has to know of the token is one 16-byte
-// record, and the loads of a batch of kMergeBatch partials (lse and values
-// together) are all in flight at once; a running maximum joins the batches.
+// Bound by the partials' bytes once many loads are in flight: a warp per token and
+// kHeads q heads, lane l with D / 32 dims of each; all it has to know of the token
+// is one 16-byte record, and the loads of kMergeBatch partials of every head (lse
+// and values together) are all in flight at once; a running maximum joins the batches.
 constexpr int kMergeBatch = 4;
-template <int D>
+template <int D, int kHeads>
 __global__ void __launch_bounds__(256)
     range_merge_kernel(PrefillArgs a, const MergeTask* __restrict__ tasks, const float* __restrict__ dec_out,
                        const float* __restrict__ dec_lse, int max_splits) {
@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(256)
     grid_wait();
     const int lane = threadIdx.x % 32;
     const int64_t job = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    const int32_t at = (int32_t)(job / a.hq), h = (int32_t)(job - (int64_t)at * a.hq);
+    const int32_t groups = a.hq / kHeads;
+    const int32_t at = (int32_t)(job / groups), h0 = (int32_t)(job - (int64_t)at * groups) * kHeads;
     if (at >= (a.num_prefixes > 0 ? a.total_q : a.num_rows)) return;
     const int4 raw = *reinterpret_cast<const int4*>(tasks + at);
     // (window calls have no prefixes, and a call without the scheduler no header)
@@ -486,51 +487,80 @@ __global__ void __launch_bounds__(256)
     const int32_t t = one ? task.token : at;
     // partials 0 .. n - 1 are the row's own keys', the others the prefix's shards
     const int n = one ? task.splits : 1, all = n + task.shards;
-    const size_t base = ((size_t)task.row * a.hq + h) * max_splits;
     const size_t out_stride = (size_t)a.total_q * a.hq * D, lse_stride = (size_t)a.hq * a.total_q;
-    const size_t li = (size_t)h * a.total_q + t, o = ((size_t)t * a.hq + h) * D;
-    float M = -INFINITY, W = 0.f, O[kV] = {};
+    float M[kHeads], W[kHeads], O[kHeads][kV] = {};
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        M[i] = -INFINITY;
+        W[i] = 0.f;
+    }
     for (int s0 = 0; s0 < all; s0 += kMergeBatch) {
-        float ls[kMergeBatch];
-        Vec x[kMergeBatch];
+        float ls[kHeads][kMergeBatch];
+        Vec x[kHeads][kMergeBatch];
 #pragma unroll
         for (int k = 0; k < kMergeBatch; ++k) {
             const int s = s0 + k;
-            ls[k] = -INFINITY;
-            if (s >= all) continue;
             const size_t p = s < n ? a.nparts - 1 : s - n;
             const bool dec = one && s < n;
-            ls[k] = __ldcg(dec ? dec_lse + base + s : a.part_lse + p * lse_stride + li);
-            x[k] = __ldcg(reinterpret_cast<const Vec*>(dec ? dec_out + (base + s) * D : a.part_out + p * out_stride + o) +
-                          lane);
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                ls[i][k] = -INFINITY;
+                if (s >= all) continue;
+                const size_t slot = ((size_t)task.row * a.hq + h0 + i) * max_splits + s;
+                ls[i][k] = __ldcg(dec ? dec_lse + slot : a.part_lse + p * lse_stride + (size_t)(h0 + i) * a.total_q + t);
+                x[i][k] = __ldcg(reinterpret_cast<const Vec*>(dec ? dec_out + slot * D
+                                                                  : a.part_out + p * out_stride +
+                                                                        ((size_t)t * a.hq + h0 + i) * D) +
+                                 lane);
+            }
         }
-        float m = M;
 #pragma unroll
-        for (int k = 0; k < kMergeBatch; ++k) m = fmaxf(m, ls[k]);
-        if (m == -INFINITY) continue;
-        const float f = __expf(M - m);
-        W *= f;
+        for (int i = 0; i < kHeads; ++i) {
+            float m = M[i];
 #pragma unroll
-        for (int e = 0; e < kV; ++e) O[e] *= f;
-        M = m;
+            for (int k = 0; k < kMergeBatch; ++k) m = fmaxf(m, ls[i][k]);
+            if (m == -INFINITY) continue;
+            const float f = __expf(M[i] - m);
+            W[i] *= f;
 #pragma unroll
-        for (int k = 0; k < kMergeBatch; ++k) {
-            if (ls[k] == -INFINITY) continue;
-            const float w = __expf(ls[k] - M);
-            W += w;
-            const float* v = reinterpret_cast<const float*>(&x[k]);
+            for (int e = 0; e < kV; ++e) O[i][e] *= f;
+            M[i] = m;
 #pragma unroll
-            for (int e = 0; e < kV; ++e) O[e] += w * v[e];
+            for (int k = 0; k < kMergeBatch; ++k) {
+                if (ls[i][k] == -INFINITY) continue;
+                const float w = __expf(ls[i][k] - m);
+                W[i] += w;
+                const float* v = reinterpret_cast<const float*>(&x[i][k]);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) O[i][e] += w * v[e];
+            }
         }
     }
-    const float inv = W > 0.f ? 1.f / W : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + o) + lane * (kV / 2);
-    if constexpr (kV == 4)
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(pack_bf16x2(O[0] * inv, O[1] * inv), pack_bf16x2(O[2] * inv, O[3] * inv));
-    else
-        *dst = pack_bf16x2(O[0] * inv, O[1] * inv);
-    if (lane == 0) a.lse[li] = W > 0.f ? M + __logf(W) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const float inv = W[i] > 0.f ? 1.f / W[i] : 0.f;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                                    ((size_t)t * a.hq + h0 + i) * D) + lane * (kV / 2);
+        if constexpr (kV == 4)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16x2(O[i][0] * inv, O[i][1] * inv), pack_bf16x2(O[i][2] * inv, O[i][3] * inv));
+        else
+            *dst = pack_bf16x2(O[i][0] * inv, O[i][1] * inv);
+        if (lane == 0)
+            a.lse[(size_t)(h0 + i) * a.total_q + t] = W[i] > 0.f ? M[i] + __logf(W[i]) : -INFINITY;
+    }
+}
+
+template <int D>
+cudaError_t launch_range_merge_d(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out,
+                                 const float* dec_lse, int32_t max_splits, cudaStream_t stream) {
+    const int heads = a.hq % 2 == 0 ? 2 : 1;
+    const int64_t jobs = (int64_t)(a.num_prefixes > 0 ? a.total_q : a.num_rows) * (a.hq / heads);
+    const dim3 grid((unsigned)((jobs + 7) / 8));
+    return heads == 2 ? launch_chained(range_merge_kernel<D, 2>, grid, dim3(256), 0, stream, a, tasks, dec_out, dec_lse,
+                                       max_splits)
+                      : launch_chained(range_merge_kernel<D, 1>, grid, dim3(256), 0, stream, a, tasks, dec_out, dec_lse,
+                                       max_splits);
 }
 
 template <int D, int GMAX, bool F8, bool RNG>
@@ -634,12 +664,8 @@ int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, in
 
 int launch_range_merge(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out, const float* dec_lse,
                        int32_t max_splits, cudaStream_t stream) {
-    const int64_t jobs = (int64_t)(a.num_prefixes > 0 ? a.total_q : a.num_rows) * a.hq;
-    const dim3 grid((unsigned)((jobs + 7) / 8));
-    const cudaError_t e = a.d == 64 ? launch_chained(range_merge_kernel<64>, grid, dim3(256), 0, stream, a, tasks, dec_out,
-                                                     dec_lse, max_splits)
-                                    : launch_chained(range_merge_kernel<128>, grid, dim3(256), 0, stream, a, tasks,
-                                                     dec_out, dec_lse, max_splits);
+    const cudaError_t e = a.d == 64 ? launch_range_merge_d<64>(a, tasks, dec_out, dec_lse, max_splits, stream)
+                                    : launch_range_merge_d<128>(a, tasks, dec_out, dec_lse, max_splits, stream);
     if (e != cudaSuccess) { set_last_cuda_error(e); return PCP_ERR_CUDA; }
     return PCP_OK;
 }

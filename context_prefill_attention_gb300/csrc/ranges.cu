@@ -95,6 +95,32 @@ RangeLayout range_layout(int32_t num_rows, int32_t num_prefixes, int32_t total_q
     return w;
 }
 
+// Workspace for a call of up to num_rows rows, num_prefixes groups and total_q tokens:
+// a smaller call can be split finer, so the parts that grow with the splits are
+// taken at their largest over all smaller calls (a caller sizes its workspace once).
+size_t range_workspace(int32_t num_rows, int32_t num_prefixes, int32_t total_q, int32_t hq, int32_t hkv, int32_t d,
+                       int64_t max_kv, int64_t max_len) {
+    const RangeLayout w = range_layout(num_rows, num_prefixes, total_q, hq, hkv, d, max_kv, max_len);
+    // decode partials and records: rows x splits
+    int64_t splits = (int64_t)num_rows * w.max_splits, most_splits = splits;
+    for (int32_t r = 1; r < num_rows; ++r) {
+        const int32_t c = decode_chunk(r, hkv, max_len);
+        const int64_t n = (int64_t)r * (max_len > 0 ? (max_len + c - 1) / c : 1);
+        if (n > most_splits) most_splits = n;
+    }
+    // partials of the prefixes and units: they change with the tokens' tiles, of one or two per item
+    int64_t parts = (int64_t)w.nparts * total_q, most_parts = parts, most_units = w.max_units;
+    const int32_t tpt = kBlockM / (hq / hkv);
+    for (int64_t t = tpt; t < total_q; t += tpt) {
+        const RangeLayout x = range_layout(0, num_prefixes, (int32_t)t, hq, hkv, d, max_kv, 0);
+        if ((int64_t)x.nparts * t > most_parts) most_parts = (int64_t)x.nparts * t;
+        if (x.max_units + num_rows > most_units) most_units = x.max_units + num_rows;
+    }
+    return w.total + (size_t)(most_splits - splits) * ((size_t)hq * (d + 1) * 4 + sizeof(DecUnit)) +
+           (size_t)(most_parts - parts) * hq * (d + 1) * 4 +
+           (size_t)(most_units - w.max_units) * 2 * sizeof(PackedUnit) + 16 * 256;
+}
+
 // Slots of the longest walk of a one-token row (KeyRange::len).
 int64_t window_len(int64_t max_kv, int32_t block_size, int32_t window, int32_t sinks) {
     const int64_t n = (int64_t)window + sinks + 2 * block_size;
@@ -238,8 +264,8 @@ extern "C" size_t pcp_attn_window_workspace_size(int32_t num_rows, int32_t total
         num_q_heads / num_kv_heads > 16 || head_dim < 1 || max_kv_len < 0 || block_size < 1 ||
         !window_ok(window, num_sinks))
         return 0;
-    return range_layout(num_rows, -1, total_q, num_q_heads, num_kv_heads, head_dim, max_kv_len,
-                        window_len(max_kv_len, block_size, window, num_sinks)).total;
+    return range_workspace(num_rows, -1, total_q, num_q_heads, num_kv_heads, head_dim, max_kv_len,
+                           window_len(max_kv_len, block_size, window, num_sinks));
 }
 
 extern "C" size_t pcp_attn_shared_prefix_workspace_size(int32_t num_rows, int32_t num_prefixes, int32_t total_q,
@@ -249,8 +275,7 @@ extern "C" size_t pcp_attn_shared_prefix_workspace_size(int32_t num_rows, int32_
         num_q_heads < num_kv_heads || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 16 || head_dim < 1 ||
         max_kv_len < 0)
         return 0;
-    return range_layout(num_rows, num_prefixes, total_q, num_q_heads, num_kv_heads, head_dim, max_kv_len, max_kv_len)
-        .total;
+    return range_workspace(num_rows, num_prefixes, total_q, num_q_heads, num_kv_heads, head_dim, max_kv_len, max_kv_len);
 }
 
 extern "C" int pcp_attn_window(const void* q, const void* key_cache, const void* value_cache,

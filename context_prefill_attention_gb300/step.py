@@ -12,6 +12,12 @@ A step ("Feat/pcp qwen36 hybrid", "Changes"; "[MRv2][PCP] Carry the row plan
    SMs ``pcp_decode_sms`` picks from the host plan, beside the prefill rows
    (``PCP_ATTN_DECODE_SMS``): a shorter step, with each kernel on part of the GPU.
 
+Step 4 is ``pcp_attn_window`` for a layer with a sliding window (``window``,
+``num_sinks``). With ``share_prefix=n`` step 1 also finds the runs of rows whose
+block tables begin with the same pages (``pcp_build_prefix_groups``, at least
+``n`` keys), and step 4 attends each such prefix once (``pcp_attn_shared_prefix``)
+when the batch has any.
+
 With ``kv_cache_dtype="fp8"`` the cache holds e4m3 codes: step 3 is
 ``pcp_kv_cache_write_fp8`` with the layer's k/v scales and step 4
 ``pcp_attn_varlen_fp8kv`` with descales of shape (num_reqs, num_kv_heads),
@@ -39,9 +45,21 @@ class PcpStep:
     def __init__(self, *, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
                  num_shards: int, split_mode: int, max_tokens: int, max_reqs: int, max_kv_len: int,
                  flags: int = 0, device: str = "cuda", kv_cache_dtype: str = "bf16", k_scale: float = 1.0,
-                 v_scale: float = 1.0, decode_beside_prefill: bool = False):
+                 v_scale: float = 1.0, decode_beside_prefill: bool = False, window: Optional[int] = None,
+                 num_sinks: int = 0, share_prefix: int = 0):
         if kv_cache_dtype not in ("bf16", "fp8"):
             raise ValueError(f"kv_cache_dtype {kv_cache_dtype!r}: 'bf16' or 'fp8'")
+        if window is not None and share_prefix:
+            raise ValueError("window and share_prefix: a layer's queries see a window or everything, not both")
+        if window is not None and (window < 1 or num_sinks < 0):
+            raise ValueError(f"window {window}, num_sinks {num_sinks}: window >= 1 and num_sinks >= 0")
+        if window is None and num_sinks:
+            raise ValueError("num_sinks needs a window")
+        if share_prefix < 0:
+            raise ValueError(f"share_prefix {share_prefix}: a number of keys, or 0")
+        if (window is not None or share_prefix) and flags:
+            raise ValueError("window and share_prefix take no attention flags")
+        self.window, self.num_sinks, self.share_prefix = window, num_sinks, share_prefix
         self.kv_fp8 = kv_cache_dtype == "fp8"
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.hq, self.hkv, self.d = num_q_heads, num_kv_heads, head_dim
@@ -54,7 +72,18 @@ class PcpStep:
         self.decode_sms = 0
         self.max_rows = max(1, 2 * num_shards * max_reqs)
         self.max_tokens = max_tokens
-        ws = L.pcp_attn_workspace_size(self.max_rows, max_tokens, num_q_heads, head_dim, max_kv_len, flags)
+        if window is not None:
+            ws = L.pcp_attn_window_workspace_size(self.max_rows, max_tokens, num_q_heads, num_kv_heads, head_dim,
+                                                  max_kv_len, block_size, window, num_sinks)
+        else:
+            ws = L.pcp_attn_workspace_size(self.max_rows, max_tokens, num_q_heads, head_dim, max_kv_len, flags)
+        self.max_groups = min(1024, self.max_rows // 2) if share_prefix else 0
+        if self.max_groups:
+            ws = max(ws, L.pcp_attn_shared_prefix_workspace_size(self.max_rows, self.max_groups, max_tokens, num_q_heads,
+                                                                 num_kv_heads, head_dim, max_kv_len))
+            self.groups_dev = torch.empty((self.max_groups, 4), dtype=torch.int32, device=self.device)
+            self.groups_host = torch.empty((self.max_groups, 4), dtype=torch.int32, pin_memory=True)
+        self.groups = np.zeros((0, 4), dtype=np.int32)
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
         self.out = torch.empty((max(max_tokens, 1), num_q_heads, head_dim), dtype=torch.bfloat16,
                                device=self.device)
@@ -80,6 +109,8 @@ class PcpStep:
                                          self.split_mode, rows_capacity=self.max_rows)
         self.decode_sms = (L.pcp_decode_sms(self.plan["rows"], self.hq, self.hkv, self.d, self.kv_fp8,
                                             self.num_sms) if self.decode_beside else 0)
+        if self.max_groups:
+            self.groups = L.pcp_build_prefix_groups(self.plan["rows"], block_table_host, self.bs, self.share_prefix)
         debug_plan(self.plan, self.shards)
         return self.plan
 
@@ -90,6 +121,10 @@ class PcpStep:
         self.slot_host[:T].numpy()[...] = p["slot_mapping"]
         self.rows_dev[:n].copy_(self.rows_host[:n], non_blocking=True)
         self.slot_dev[:T].copy_(self.slot_host[:T], non_blocking=True)
+        g = self.groups.shape[0]
+        if g:
+            self.groups_host[:g].numpy()[...] = self.groups
+            self.groups_dev[:g].copy_(self.groups_host[:g], non_blocking=True)
 
     def write_cache(self, k_new: torch.Tensor, v_new: torch.Tensor, key_cache: torch.Tensor,
                     value_cache: torch.Tensor, stream=None) -> None:
@@ -107,6 +142,16 @@ class PcpStep:
         n = int(self.plan["rows"].shape[0])
         out = self.out[:T]
         lse = self.lse_buf[:T * self.hq].view(self.hq, T)
+        if self.window is not None or self.groups.shape[0]:
+            kw = dict(out=out, lse=lse, workspace=self.workspace, status=self.status, stream=stream)
+            R = int(block_table_dev.shape[0])
+            descales = (self.k_descale[:R], self.v_descale[:R]) if self.kv_fp8 else ()
+            head = (q, key_cache, value_cache, *descales, block_table_dev, self.rows_dev[:n])
+            if self.window is not None:
+                f = L.pcp_attn_window_fp8kv if self.kv_fp8 else L.pcp_attn_window
+                return f(*head, scale, self.window, self.num_sinks, **kw)
+            f = L.pcp_attn_shared_prefix_fp8kv if self.kv_fp8 else L.pcp_attn_shared_prefix
+            return f(*head, self.groups_dev[:self.groups.shape[0]], scale, **kw)
         flags = self.flags | L.PCP_ATTN_DECODE_SMS(self.decode_sms)
         if self.kv_fp8:
             R = int(block_table_dev.shape[0])

@@ -364,7 +364,8 @@ int pcp_attn_varlen_fp8kv(const void* q, const void* key_cache, const void* valu
  * Every other argument, limit, check and error is that of pcp_attn_varlen;
  * there are no flags. workspace: at least pcp_attn_window_workspace_size(
  * num_rows, total_q, Hq, Hkv, D, max_blocks_per_req * block_size, block_size,
- * window, num_sinks) bytes. Errors: PCP_ERR_ARG also for window < 1 or
+ * window, num_sinks) bytes, which is enough for every call of fewer rows and
+ * tokens too. Errors: PCP_ERR_ARG also for window < 1 or
  * num_sinks < 0.
  * pcp_attn_window_fp8kv: the same over an FP8 (e4m3) cache, with the descales
  * and numerics of pcp_attn_varlen_fp8kv.
@@ -426,7 +427,8 @@ int pcp_build_prefix_groups(const pcp_row_t* rows, int32_t num_rows, const int32
  * only (see pcp_attn_window). FP8 cache: the descales of a prefix are those of its req.
  * Every other argument, limit, check and error is that of pcp_attn_varlen; there
  * are no flags. workspace: at least pcp_attn_shared_prefix_workspace_size(
- * num_rows, num_prefixes, total_q, Hq, Hkv, D, max_blocks_per_req * block_size) bytes.
+ * num_rows, num_prefixes, total_q, Hq, Hkv, D, max_blocks_per_req * block_size)
+ * bytes, which is enough for every call of fewer rows, groups and tokens too.
  */
 size_t pcp_attn_shared_prefix_workspace_size(int32_t num_rows, int32_t num_prefixes, int32_t total_q,
                                              int32_t num_q_heads, int32_t num_kv_heads,

@@ -303,3 +303,33 @@ def test_binding_needs_device_tensors(P):
         P.pcp_attn_window(q, c, c, bt, rows, 0.1, 8, stream=0)
     with pytest.raises(ValueError, match="CUDA"):
         P.pcp_kv_release(bt, bt[:, 0].contiguous(), bt[:, 0].contiguous(), bt[0], stream=0)
+
+
+def test_workspace_covers_smaller_calls(P):
+    """Sized once for the largest call: fewer rows, groups or tokens never need more."""
+    rng = np.random.default_rng(0)
+    for _ in range(60):
+        hkv = int(rng.choice([1, 2, 8]))
+        hq, d, bs = hkv * int(rng.choice([1, 3, 4, 16])), int(rng.choice([64, 128])), int(rng.choice([8, 16, 128]))
+        kv = int(2 ** rng.uniform(3, 17))
+        T = int(2 ** rng.uniform(0, 13))
+        n = int(rng.integers(1, T + 1))
+        t = int(rng.integers(1, T + 1))
+        m = int(rng.integers(1, min(n, t) + 1))
+        w = int(2 ** rng.uniform(0, 14))
+        big = P.pcp_attn_window_workspace_size(n, T, hq, hkv, d, kv, bs, w, 4)
+        assert P.pcp_attn_window_workspace_size(m, t, hq, hkv, d, kv, bs, w, 4) <= big, (n, T, m, t, hq, hkv, kv, w)
+        g = int(rng.integers(1, 20))
+        big = P.pcp_attn_shared_prefix_workspace_size(n, g, T, hq, hkv, d, kv)
+        for g2 in (0, int(rng.integers(0, g + 1))):
+            assert P.pcp_attn_shared_prefix_workspace_size(m, g2, t, hq, hkv, d, kv) <= big, (n, g, T, m, g2, t, hq, hkv, kv)
+
+
+def test_step_refuses_what_does_not_go_together(P):
+    kw = dict(num_q_heads=8, num_kv_heads=2, head_dim=128, block_size=16, num_shards=1, split_mode=0, max_tokens=8,
+              max_reqs=2, max_kv_len=64)
+    for bad in (dict(window=0), dict(window=4, num_sinks=-1), dict(num_sinks=2), dict(window=4, share_prefix=8),
+                dict(share_prefix=-1), dict(window=4, flags=P.PCP_ATTN_SEPARATE_CONTEXT),
+                dict(share_prefix=8, flags=P.PCP_ATTN_KV_SHARDS(2))):
+        with pytest.raises(ValueError):
+            P.PcpStep(**kw, **bad)
