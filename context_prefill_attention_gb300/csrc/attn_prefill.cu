@@ -1615,7 +1615,10 @@ __global__ void __launch_bounds__(NT, 1)
         __syncthreads();
     }
     const int32_t n = (int32_t)min((int64_t)base, max_units);
-    if (tid == 0) header[0] = n;
+    if (tid == 0) {
+        header[0] = n;
+        if (base > max_units) report_status(a.status, PCP_ERR_RANGE);  // rows that share tokens
+    }
     if (n > 0) {
         // longest first (units of one class in any order: an item writes only its own
         // results, which do not depend on its place)

@@ -163,7 +163,7 @@ int range_call(const RangeCall& c) {
         return PCP_ERR_ALIGN;
     if (c.num_blocks * (int64_t)c.block_size > INT32_MAX || (int64_t)c.total_q * c.hq > INT32_MAX) return PCP_ERR_ARG;
     const int64_t max_kv = (int64_t)c.max_blocks * c.block_size;
-    if (max_kv > INT32_MAX) return PCP_ERR_ARG;
+    if (max_kv > INT32_MAX - 1024) return PCP_ERR_ARG;  // positions are rounded up to tiles and pages in 32 bits
     const bool shared = c.num_prefixes >= 0;
     const int64_t max_len = shared ? max_kv : window_len(max_kv, c.block_size, c.window, c.sinks);
     const RangeLayout w = range_layout(c.num_rows, c.num_prefixes, c.total_q, c.hq, c.hkv, c.d, max_kv, max_len);

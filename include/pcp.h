@@ -361,11 +361,12 @@ int pcp_attn_varlen_fp8kv(const void* q, const void* key_cache, const void* valu
  * A row of one token takes the decode path whatever its is_decode. The rows'
  * tokens are disjoint, so a call with num_rows >= total_q has one-token rows
  * only: any longer row in it is refused (skipped, *status = PCP_ERR_RANGE).
- * Every other argument, limit, check and error is that of pcp_attn_varlen;
+ * Every other argument, limit, check and error is that of pcp_attn_varlen (and
+ * max_blocks_per_req * block_size at most 2^31 - 1024);
  * there are no flags. workspace: at least pcp_attn_window_workspace_size(
  * num_rows, total_q, Hq, Hkv, D, max_blocks_per_req * block_size, block_size,
  * window, num_sinks) bytes, which is enough for every call of fewer rows and
- * tokens too. Errors: PCP_ERR_ARG also for window < 1 or
+ * tokens too; calls that may overlap on the GPU need one each. Errors: PCP_ERR_ARG also for window < 1 or
  * num_sinks < 0.
  * pcp_attn_window_fp8kv: the same over an FP8 (e4m3) cache, with the descales
  * and numerics of pcp_attn_varlen_fp8kv.
@@ -428,7 +429,8 @@ int pcp_build_prefix_groups(const pcp_row_t* rows, int32_t num_rows, const int32
  * Every other argument, limit, check and error is that of pcp_attn_varlen; there
  * are no flags. workspace: at least pcp_attn_shared_prefix_workspace_size(
  * num_rows, num_prefixes, total_q, Hq, Hkv, D, max_blocks_per_req * block_size)
- * bytes, which is enough for every call of fewer rows, groups and tokens too.
+ * bytes, which is enough for every call of fewer rows, groups and tokens too; calls
+ * that may overlap on the GPU need one each.
  */
 size_t pcp_attn_shared_prefix_workspace_size(int32_t num_rows, int32_t num_prefixes, int32_t total_q,
                                              int32_t num_q_heads, int32_t num_kv_heads,

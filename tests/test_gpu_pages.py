@@ -291,3 +291,23 @@ def test_serving_run_fork_share_evict_compact():
     after = P.pcp_attn_window(q, k, v, table, rows, b.scale, window, sinks, status=st)
     assert torch.equal(before[0], after[0]) and torch.equal(before[1], after[1])
     assert int(st.item()) == 0
+
+
+def test_pages_beyond_32_bits_of_bytes():
+    """Copies between pages that lie more than 2^32 bytes apart."""
+    P = _pcp()
+    nb, bs = 140000, 16  # 32 KB pages: 4.6 GB
+    k = torch.zeros((nb, bs, 8, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    ref = np.ones(nb, dtype=np.int32)
+    ref[7] = 0
+    k[nb - 1], v[nb - 1] = 3, 5
+    table = np.array([[nb - 1]], dtype=np.int32)
+    t, r = P.pcp_kv_fork(k, v, _cuda(table), _cuda([5]), _cuda([0]), _cuda(ref))
+    assert t.tolist() == [[7]] and bool((k[7, :5] == 3).all()) and bool((v[7, :5] == 5).all())
+    assert not bool(k[7, 5:].any()) and int(r[7]) == 1
+    ref[:] = 0
+    ref[nb - 1] = 2
+    t, r, live = P.pcp_kv_compact(k, v, _cuda(table), _cuda(ref))
+    assert t.tolist() == [[0]] and int(live.item()) == 1 and int(r[0]) == 2 and int(r[nb - 1]) == 0
+    assert bool((k[0] == 3).all()) and bool((v[0] == 5).all()) and not bool(k[1].any())

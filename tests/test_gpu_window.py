@@ -142,3 +142,49 @@ def test_random_batches(seed):
               sinks=int(rng.choice([0, 1, 4, 50, 200])), seed=seed, pad=int(rng.integers(3)),
               split_rows=bool(rng.integers(2)))
     b.check(*b.run())
+
+
+def test_two_streams_with_a_workspace_each():
+    P = _pcp()
+    batches = [Batch(MIXED, 8, 2, 128, 16, window=100, sinks=4, seed=s) for s in (21, 22)]
+    want = [b.run() for b in batches]
+    torch.cuda.synchronize()
+    got = [b.buffers() for b in batches]
+    ws = [torch.empty(P.pcp_attn_window_workspace_size(len(b.rows), b.T, 8, 2, 128, b.table.shape[1] * 16, 16, 100, 4),
+                      dtype=torch.uint8, device="cuda") for b in batches]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for b, s, (o, l), w in zip(batches, streams, got, ws):
+            b.run(out=o, lse=l, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for (o, l), (o2, l2) in zip(got, want):
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp8_query_out_of_range_is_reported(d):
+    """An element of q beyond +-65504 in a decode or a longer row; not one in a token of no row."""
+    P = _pcp()
+    for tok, status in ((0, P.PCP_ERR_RANGE if d == 128 else 0), (3, P.PCP_ERR_RANGE), (1, 0), (43, 0)):
+        b = Batch([(1, 50), (40, 20)], 8, 2, d, 16, fp8=True, window=30, sinks=2, seed=3, pad=2)
+        b.q_dev[tok, 5, 7] = 1e5
+        b.run()
+        torch.cuda.synchronize()
+        assert int(b.status.item()) == status, (tok, d)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_beyond_32_bits_of_elements(fp8):
+    """The pages lie at the end of caches of more than 2^32 elements each."""
+    b = Batch([(1, 700), (70, 300), (1, 0)], 32, 8, 128, 16, fp8=fp8, window=256, sinks=4, seed=9)
+    big = (1 << 32) // (16 * 8 * 128) + 10
+    shape = (big, 16, 8, 128)
+    move = big - b.nb
+    caches = []
+    for c in (b.kc, b.vc):
+        x = torch.empty(shape, dtype=c.dtype, device="cuda")
+        x[move:] = c
+        caches.append(x)
+    b.kc, b.vc = caches
+    b.table_dev = torch.where(b.table_dev >= 0, b.table_dev + move, -1).to(torch.int32)
+    b.check(*b.run())
