@@ -311,3 +311,46 @@ def test_pages_beyond_32_bits_of_bytes():
     t, r, live = P.pcp_kv_compact(k, v, _cuda(table), _cuda(ref))
     assert t.tolist() == [[0]] and int(live.item()) == 1 and int(r[0]) == 2 and int(r[nb - 1]) == 0
     assert bool((k[0] == 3).all()) and bool((v[0] == 5).all()) and not bool(k[1].any())
+
+
+@pytest.mark.parametrize("nb", [16384, 16385, 131073])
+def test_pool_sizes_around_the_one_cluster_form(nb):
+    """Fork (16 and 17 children, and none), release and compaction at the largest pool that one
+    cluster takes and one page more."""
+    P = _pcp()
+    rng = np.random.default_rng(nb)
+    bs = 2
+    lens = rng.integers(0, 40, 30).tolist()
+    table, ref = _layout(rng, lens, bs, nb)
+    ref[rng.random(nb) < 0.4] += 1
+    caches = _pool(nb, bs, 1, 16, torch.uint8, 3)
+    for kids in (0, 16, 17):
+        parent = rng.integers(0, 30, kids).tolist()
+        dev = [c.cuda() for c in caches]
+        t, r = P.pcp_kv_fork(*dev, _cuda(table), _cuda(lens), _cuda(parent), _cuda(ref))
+        want, wt, wr = _fork(caches, table, lens, parent, ref, bs)
+        _check([t, r], [wt, wr])
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(dev, want))
+    need = [-(-n // bs) for n in lens]
+    t, r = P.pcp_kv_release(_cuda(table), _cuda([0] * 30), _cuda(need), _cuda(ref))
+    wr = ref.copy()
+    for row, k in zip(table, need):
+        wr[row[:k]] -= 1
+    _check([t, r], [np.full_like(table, -1), wr])
+    dev = [c.cuda() for c in caches]
+    t, r, live = P.pcp_kv_compact(*dev, _cuda(table), _cuda(ref))
+    want, wt, wr, n = _compact(caches, table, ref)
+    _check([t, r], [wt, wr])
+    assert int(live.item()) == n and all(torch.equal(a.cpu(), b) for a, b in zip(dev, want))
+
+
+def test_release_of_many_entries():
+    """More table entries than one cluster takes."""
+    P = _pcp()
+    R, mb, nb = 60, 512, 1000
+    table = np.arange(R * mb, dtype=np.int32).reshape(R, mb) % nb
+    ref = np.bincount(table.reshape(-1), minlength=nb).astype(np.int32)
+    t, r = P.pcp_kv_release(_cuda(table), _cuda([1] * R), _cuda([mb] * R), _cuda(ref))
+    want = table.copy()
+    want[:, 1:] = -1
+    _check([t, r], [want, np.bincount(table[:, 0], minlength=nb)])
