@@ -13,7 +13,8 @@
 //    warpgroup, their tiles interleaved in one stream (tile j of the first, tile j of
 //    the second, ...): the rings, the MMA issuers and the converters follow that stream,
 //    and one item's start and end run under the other's tiles. Measured against the
-//    shared items: TODO;
+//    shared items: 64 rows of 16 to 512 keys on 61 SMs 39 -> 31 us, 128 rows of 4132
+//    slots over an e4m3 cache 219 -> 214 us (4.8 TB/s);
 //  * an item has one partial, or is the row's result itself where the call's rows
 //    are one split each (a.direct);
 //  * each warpgroup has its own S, P and O buffer; Q^T has two buffers per
@@ -23,7 +24,11 @@
 // Launched behind the scheduler (launch_chained), on header[2] of the SMs. A call of
 // a few one-token rows whose items all fit the SMs at once (a.inline_items) has no
 // scheduler: one warp of each CTA reads the rows (kInlineRows at most) and finds
-// the CTA's two items itself. Measured, 4 rows with a window of 1024: TODO us.
+// the CTA's two items itself. Measured, 4 rows with a window of 1024: 18.5 -> 16.4 us.
+//
+// What bounds it: HBM with a bf16 cache where the rows fill the SMs (56 rows of 1060
+// slots: 242 MB in 46 us, 5.3 TB/s), the widening of V and the tiles' latency over an
+// e4m3 one (64 % of the DRAM cycles), the latency of one pair of items in small calls.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

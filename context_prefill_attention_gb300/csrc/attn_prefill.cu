@@ -190,6 +190,12 @@ __device__ __forceinline__ Item decode_item(const Unit* units, int32_t idx, int3
 // pages back to back: those of the sinks that lie before the window, then those
 // from the window's first key on. Slot v of that walk is key v below the sinks'
 // last page end, key v + shift after it.
+//
+// What bounds the packed kernel: per item of two tiles about 4 us in which the tensor
+// pipe waits (the last tile's softmax, O's way out, the first tile's), 3 us for edges and
+// stores, and 1.7 us per 128-key tile, the pace of the issuing thread (as in the
+// plain form). Measured with 8 x 8192 tokens, 32 q / 8 kv heads, D = 128: window 64 6.9 us
+// per item, 1024 20.4 us (937 TFLOP/s of visible pairs), 8192 62.5 us (1299).
 __device__ __forceinline__ PackedUnit packed_unit(const PrefillArgs& a, int32_t req, int32_t q_start, int32_t q_len,
                                                   int32_t first_pos, int32_t mt, int32_t span, int32_t k_lo,
                                                   int32_t k_hi, int32_t pass) {
