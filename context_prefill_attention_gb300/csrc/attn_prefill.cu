@@ -370,7 +370,8 @@ __device__ __forceinline__ float q_row_to_e4m3(uint8_t* tile, int r, bool* over)
 // add of a constant (the issuing thread's instruction count per MMA is on the
 // critical path of the tensor pipe).
 template <int D, bool F8>
-__device__ __forceinline__ void issue_qk(uint32_t tmem_s, uint64_t q_desc, uint64_t k_desc) {
+__device__ __forceinline__ void issue_qk(uint32_t tmem_s, uint64_t q_desc, uint64_t k_desc,
+                                         uint32_t idesc = Cfg<D, F8>::kIdescS) {
     if constexpr (Cfg<D, F8>::kE4) {
         // e4m3: q's two term tiles (term t at + t * kHalfBytes) against the K codes,
         // 32 dims (32 bytes of each 128-byte row) per MMA: the same 8 MMAs
@@ -379,12 +380,12 @@ __device__ __forceinline__ void issue_qk(uint32_t tmem_s, uint64_t q_desc, uint6
 #pragma unroll
             for (int ks = 0; ks < D / 32; ++ks)
                 mma_ss_e4m3(tmem_s, q_desc + (uint32_t)((t * Cfg<D>::kHalfBytes + ks * 32) >> 4),
-                            k_desc + (uint32_t)(ks * 2), Cfg<D, F8>::kIdescS, (t | ks) ? 1u : 0u);
+                            k_desc + (uint32_t)(ks * 2), idesc, (t | ks) ? 1u : 0u);
     } else {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks / 4) * Cfg<D>::kHalfBytes + (ks % 4) * 32) >> 4;
-            mma_ss(tmem_s, q_desc + off, k_desc + off, Cfg<D, F8>::kIdescS, ks > 0 ? 1u : 0u);
+            mma_ss(tmem_s, q_desc + off, k_desc + off, idesc, ks > 0 ? 1u : 0u);
         }
     }
 }
@@ -679,6 +680,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item it = item_at(idx);
             const int n = it.n_tiles;
             if (n == 0) continue;
+            // PACK: S negated where scale (and an e4m3 cache's K descale) is negative
+            uint32_t idesc = C::kIdescS;
+            if constexpr (PACK) {
+                const float kd = F8 ? __ldg(a.k_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
+                if (a.scale * kd < 0.f) idesc |= kNegateA;
+            }
             if (!(ok = mbar_wait(q_full, c & 1, abort_flag))) break;
             int ks = kt % kNK;
             // K(0) (bf16: with V(0))
@@ -687,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             tc_fence_after();
             for (int g = 0; g < it.nslots; ++g) {
-                issue_qk<D, F8>(tmem + C::tmem_s(g), g ? qd1 : qd0, k_desc(ks));
+                issue_qk<D, F8>(tmem + C::tmem_s(g), g ? qd1 : qd0, k_desc(ks), idesc);
                 mma_commit(s_full(g));
             }
             ++kt;
@@ -725,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 break;
                             tc_fence_after();
                         }
-                        issue_qk<D, F8>(tmem + C::tmem_s(g), g ? qd1 : qd0, k_desc(ks));
+                        issue_qk<D, F8>(tmem + C::tmem_s(g), g ? qd1 : qd0, k_desc(ks), idesc);
                         mma_commit(s_full(g));
                         if (g == it.nslots - 1) ++kt;
                     } else {
@@ -802,7 +809,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 uint32_t s[128];
                 float* sf = reinterpret_cast<float*>(s);
-                const float sl2 = F8 ? a.scale * __ldg(kd_ptr) * kLog2e * qs_row : a.scale * kLog2e;
+                const float sl2_signed = F8 ? a.scale * __ldg(kd_ptr) * kLog2e * qs_row : a.scale * kLog2e;
+                // PACK: under a negative scale S comes negated (kNegateA), so that the row's
+                // maximum is that of the scaled scores; a scale of zero is lifted off it, so
+                // that the -inf of a masked key stays one
+                const float sl2 = PACK ? fmaxf(fabsf(sl2_signed), 1e-37f) : sl2_signed;
                 const int32_t key0 = PACK ? j * kBlockN : it.kb + j * kBlockN;
                 const bool full = PACK ? key0 >= full_lo && key0 + kBlockN <= full_hi
                                        : key0 >= it.k_lo && key0 + kBlockN <= it.k_hi && key0 + kBlockN - 1 <= it.pos0;

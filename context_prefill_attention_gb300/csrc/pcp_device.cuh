@@ -187,6 +187,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
            | ((uint32_t)(M >> 4) << 24);             // M / 16
 }
 
+// Instruction descriptor bit: A negated.
+constexpr uint32_t kNegateA = 1u << 13;
+
 // Instruction descriptor of kind::f16 with f16 A and B, fp32 D.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
     return (1u << 4)                                 // D format: f32

@@ -8,7 +8,10 @@ accumulation of 128 products is off by at most 128 x 2^-23 x scale x sum |q k| (
 for N(0, 1) inputs, twice in p / sum p), over an FP8 cache q's two e4m3 terms
 drop at most 2^-17 of the row's largest element (|q| <= 6, sum |k| <= 128 x 1.2: 128 x 2^-17 x 6
 x 1.2 x scale = 6e-4), and the exponentials are good to 2^-21. The same exponent errors bound
-the LSE, held to the 1e-3 that pcp_attn_varlen is held to.
+the LSE, held to the 1e-3 that pcp_attn_varlen is held to. An f16 weight (e4m3
+cache) is a multiple of 2^-24 below 2^-14, so it is off by up to 2^-25 there, with
+the largest weight of its row 1 or more and the sum p at least that: 2^-25 sum |v|
+over the visible keys besides (it shows where the weights that matter meet v = 0).
 """
 import math
 
@@ -136,7 +139,8 @@ class Batch:
         """out, lse and the error bound, fp64, zero where no row is."""
         dev = "cuda"
         out = torch.zeros((self.T, self.hq, self.d), dtype=torch.float64, device=dev)
-        tol, lse = torch.zeros_like(out), torch.zeros((self.hq, self.T), dtype=torch.float64, device=dev)
+        tol, tiny = torch.zeros_like(out), torch.zeros_like(out)
+        lse = torch.zeros((self.hq, self.T), dtype=torch.float64, device=dev)
         G = self.hq // self.hkv
         for req, _, t0, n, _, end, _, _ in self.rows.tolist():
             K, V = (self.keys[i][req][:end].double().to(dev) for i in range(2))
@@ -150,8 +154,10 @@ class Batch:
                 w = torch.exp(x - z[:, None])
                 out[t0:t0 + n, h] = w @ V[:, h // G]
                 tol[t0:t0 + n, h] = w @ V[:, h // G].abs()
+                if self.fp8:
+                    tiny[t0:t0 + n, h] = 2.0 ** -25 * (seen.double() @ V[:, h // G].abs())
                 lse[h, t0:t0 + n] = z
-        return out, lse, out.abs() * 2.0 ** -8 + tol * (2.0 ** -8 + 2.0 ** -10)
+        return out, lse, out.abs() * 2.0 ** -8 + tol * (2.0 ** -8 + 2.0 ** -10) + tiny
 
     def covered(self):
         m = torch.zeros(self.T, dtype=torch.bool, device="cuda")

@@ -188,3 +188,52 @@ def test_pages_beyond_32_bits_of_elements(fp8):
     b.kc, b.vc = caches
     b.table_dev = torch.where(b.table_dev >= 0, b.table_dev + move, -1).to(torch.int32)
     b.check(*b.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("scale", [-0.4, 0.0, -3.0])
+def test_scales_of_either_sign(scale, fp8):
+    """Negative scales (scores of up to 100 and more) and zero."""
+    for d in (128, 64):
+        b = Batch([(70, 200), (1, 333), (5, 1), (200, 0)], 8, 2, d, 16, fp8=fp8, window=150, sinks=3, seed=7)
+        b.scale = scale
+        out, lse = b.run()
+        torch.cuda.synchronize()
+        assert int(b.status.item()) == 0 and torch.isfinite(out).all() and torch.isfinite(lse).all()
+        # the scores' own errors grow with the scale: those of the bound's 1 / sqrt(d), times the ratio
+        ref, rl, tol = b.reference()
+        worst = 2.0 ** -10 * abs(scale) * d ** 0.5
+        wide = tol + worst * (tol / (2.0 ** -8 + 2.0 ** -10))
+        assert ((out.double() - ref).abs() <= wide).all()
+        assert ((lse.double() - rl).abs() <= 1e-3 * max(1.0, abs(scale) * d ** 0.5)).all()
+
+
+def test_rising_and_huge_scores():
+    """Scores that grow along the keys by far more than the softmax's lazy rescaling takes."""
+    b = Batch([(130, 500), (1, 700)], 8, 2, 128, 16, window=400, sinks=4, seed=8)
+    flat = b.kc.view(-1, 2, 128)
+    for r, (n, c) in enumerate(b.reqs):
+        end = n + c
+        gain = torch.linspace(0.1, 6.0, end, dtype=torch.float64)[:, None, None]
+        grown = (b.keys[0][r].double() * gain).to(torch.bfloat16)
+        lo = max(0, c - 400 + 1)
+        for p in range(end):
+            if p < 4 or p >= lo:
+                flat[int(b.table[r, p // 16]) * 16 + p % 16] = grown[p].cuda()
+        b.keys[0][r] = grown
+    out, lse = b.run()
+    torch.cuda.synchronize()
+    ref, rl, tol = b.reference()
+    wide = tol + 6 * 2.0 ** -10 * (tol / (2.0 ** -8 + 2.0 ** -10))  # keys of up to six times the bound's
+    assert ((out.double() - ref).abs() <= wide).all()
+    assert ((lse.double() - rl).abs() <= 6e-3).all()
+
+
+def test_negative_descales():
+    b = Batch([(70, 200), (1, 333), (200, 0)], 8, 2, 128, 16, fp8=True, window=150, sinks=3, seed=17)
+    for x, dev in ((b.kd, b.kd_dev), (b.vd, b.vd_dev)):
+        x[:, 1] *= -1
+        dev.copy_(x)
+    b.keys = [[c.double() * s[r].double()[:, None] for r, c in enumerate(cs)]
+              for cs, s in zip(b.codes, (b.kd, b.vd))]
+    b.check(*b.run())
