@@ -11,12 +11,20 @@
 // both wait; here each warpgroup has an item of its own:
 //  * a CTA takes its items two at a time (items 2q and 2q + 1 of its share), one per
 //    warpgroup, their tiles interleaved in one stream (tile j of the first, tile j of
-//    the second, ...): the rings, the MMA issuers and the converters follow that stream,
+//    the second, ...): the rings, the MMA issuers and the q warps follow that stream,
 //    and one item's start and end run under the other's tiles. Measured against the
 //    shared items: 64 rows of 16 to 512 keys on 61 SMs 39 -> 31 us, 128 rows of 4132
-//    slots over an e4m3 cache 219 -> 214 us (4.8 TB/s);
+//    slots over an e4m3 cache 219 -> 214 us;
 //  * an item has one partial, or is the row's result itself where the call's rows
 //    are one split each (a.direct);
+//  * e4m3 cache: PV takes the V codes as they are too (A MN-major, 32 keys per MMA):
+//    P goes in as three e4m3 terms, p 2^8, then the remainder 2^12, then its remainder
+//    2^16 (each term keeps 4 significant bits, so a remainder is at most 2^-4 of what it
+//    remains of and stays below e4m3's 448), in columns of their own, whose O^T the
+//    softmax joins with the powers of two taken back: 12 significant bits of p, and
+//    2^-26 of the row's largest weight where a term is subnormal. No V is widened, and
+//    the rings hold six 16 KB tiles of K and of V. Measured against V widened to f16
+//    by converter warps: 128 rows of 4132 slots 214 -> 182 us (5.7 TB/s);
 //  * each warpgroup has its own S, P and O buffer; Q^T has two buffers per
 //    warpgroup (one with 16 heads, for lack of shared memory);
 //  * the producers look one tile ahead: a tile's pages, and behind an item's last
@@ -27,8 +35,8 @@
 // the CTA's two items itself. Measured, 4 rows with a window of 1024: 18.5 -> 16.4 us.
 //
 // What bounds it: HBM with a bf16 cache where the rows fill the SMs (56 rows of 1060
-// slots: 242 MB in 46 us, 5.3 TB/s), the widening of V and the tiles' latency over an
-// e4m3 one (64 % of the DRAM cycles), the latency of one pair of items in small calls.
+// slots: 242 MB in 46 us, 5.3 TB/s; 128 of 4132 over an e4m3 cache: 1.04 GB in 182 us,
+// 5.7 TB/s, 84 % of a copy's), the latency of one pair of items in small calls.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,20 +55,21 @@ namespace {
 template <bool F8, int GP>
 struct PairCfg {
     static constexpr int kNS = 16;                     // S^T columns: the q heads, or their e4m3 terms
-    static constexpr int kGS = GP <= 8 ? 8 : 16;       // head stride; O^T columns: P's hi parts, then the remainders
-    static constexpr int kNO = 2 * kGS;
-    static constexpr int kKS = F8 ? 4 : 3;             // K tiles in flight
-    static constexpr int kVS = (F8 && GP <= 4) ? 4 : 3;  // V tiles in flight
+    static constexpr int kGS = GP <= 8 ? 8 : 16;       // head stride of the per-head arrays
+    // O^T columns, P^T rows: P's hi parts, then the remainders (bf16: two terms; e4m3: three)
+    static constexpr int kTS = F8 ? (GP <= 4 ? 4 : 8) : kGS;  // columns per term
+    static constexpr int kNO = F8 ? (GP <= 4 ? 16 : 32) : 2 * kGS;
+    static constexpr int kKS = F8 ? 6 : 3;             // K tiles in flight
+    static constexpr int kVS = F8 ? 6 : 3;             // V tiles in flight
     static constexpr int kQB = GP <= 8 ? 2 : 1;        // Q^T buffers per warpgroup
     static constexpr int kHalfBytes = kKeys * 128;
-    static constexpr int kTileBytes = 2 * kHalfBytes;
-    static constexpr int kKTileBytes = F8 ? kHalfBytes : kTileBytes;
+    static constexpr int kTileBytes = F8 ? kHalfBytes : 2 * kHalfBytes;  // 128 keys x 128 dims
     static constexpr int kRowsBytes = kN * 128;
     static constexpr int kQBytes = 2 * kRowsBytes;
     static constexpr int kQCBytes = F8 ? kNS * 128 : 0;
-    static constexpr int kPBytes = 2 * kNO * 128;
+    static constexpr int kPBytes = (F8 ? 1 : 2) * kNO * 128;
     static constexpr int kK = 0;
-    static constexpr int kV = kKS * kKTileBytes;
+    static constexpr int kV = kKS * kTileBytes;
     static constexpr int kQ = kV + kVS * kTileBytes;   // [warpgroup + 2 x buffer]
     static constexpr int kQC = kQ + 2 * kQB * kQBytes;
     static constexpr int kP = kQC + 2 * kQB * kQCBytes;
@@ -71,14 +80,15 @@ struct PairCfg {
     // needs the softmax in pair q + 1, past its reading of pair q's
     static constexpr int kQs = kSum + 2 * 2 * 4 * kGS * 4;
     static constexpr int kBar = kQs + 8 * kGS * 4;
-    static constexpr int kNumBars = 2 * kKS + 3 * kVS + 3 * 2 * kQB + 8 + 4 * 2;
+    static constexpr int kNumBars = 2 * kKS + 2 * kVS + 3 * 2 * kQB + 8 + 4 * 2;
+    static constexpr int kThreads = 32 * (F8 ? 16 : 12);  // e4m3: four warps turn q into its terms
     static constexpr int kMisc = kBar + kNumBars * 8;  // TMEM address, abort flag, item count
     static constexpr int kOwn = kMisc + 16;            // PairItem [2]: a.inline_items
     static constexpr int kSmem = kOwn + 2 * 40 + 1024;  // + alignment slack
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * kNS;
     static constexpr uint32_t kTmemCols = 2 * kNS + 2 * kNO <= 64 ? 64 : 128;
     static constexpr uint32_t kIdescS = F8 ? idesc_e4m3(128, kNS) : idesc_bf16(128, kN, false, false);
-    static constexpr uint32_t kIdescO = F8 ? idesc_f16(128, kNO, true, false) : idesc_bf16(128, kNO, true, false);
+    static constexpr uint32_t kIdescO = F8 ? idesc_e4m3(128, kNO, true) : idesc_bf16(128, kNO, true, false);
 };
 static_assert(PairCfg<true, 4>::kSmem <= 232448 && PairCfg<true, 8>::kSmem <= 232448 &&
                   PairCfg<false, 8>::kSmem <= 232448 && PairCfg<false, 16>::kSmem <= 232448, "shared memory");
@@ -186,27 +196,25 @@ __device__ __forceinline__ int32_t inline_items(const PrefillArgs& a, int32_t p0
 }
 
 template <bool F8, int GP>
-__global__ void __launch_bounds__(tc_threads(F8, GP), 1)
+__global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
     decode_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, PrefillArgs a, float* __restrict__ dec_out,
                        float* __restrict__ dec_lse, int max_splits, int q_rows) {
     using C = PairCfg<F8, GP>;
-    constexpr int kKS = C::kKS, kVS = C::kVS, kNS = C::kNS, kGS = C::kGS, kNO = C::kNO, kQB = C::kQB;
+    constexpr int kKS = C::kKS, kVS = C::kVS, kNS = C::kNS, kGS = C::kGS, kNO = C::kNO, kQB = C::kQB, kTS = C::kTS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + C::kBar;
-    // stage barriers: K tile landed, K stage free (its S is done); V tile ready (FP8:
-    // widened), V stage free (its PV is done), FP8 V codes landed
+    // stage barriers: K tile landed, K stage free (its S is done); V the same (its PV)
     auto k_full = [&](int s) { return bar0 + 8 * s; };
     auto k_empty = [&](int s) { return bar0 + 8 * (kKS + s); };
     const uint32_t bv = bar0 + 8 * 2 * kKS;
     auto v_full = [&](int s) { return bv + 8 * s; };
     auto v_empty = [&](int s) { return bv + 8 * (kVS + s); };
-    auto vc_full = [&](int s) { return bv + 8 * (2 * kVS + s); };
     // per Q^T buffer: ready / bf16 landed (FP8) / free; FP8: q scales of a slot written
-    const uint32_t bq = bv + 8 * 3 * kVS;
+    const uint32_t bq = bv + 8 * 2 * kVS;
     auto q_full = [&](int b) { return bq + 8 * b; };
     auto qc_full = [&](int b) { return bq + 8 * (2 * kQB + b); };
     auto q_empty = [&](int b) { return bq + 8 * (4 * kQB + b); };
@@ -230,9 +238,8 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
             mbar_init(k_empty(s), 1);
         }
         for (int s = 0; s < kVS; ++s) {
-            mbar_init(v_full(s), filled);
+            mbar_init(v_full(s), 1);
             mbar_init(v_empty(s), 1);
-            mbar_init(vc_full(s), 1);
         }
         for (int b = 0; b < 2 * kQB; ++b) {
             mbar_init(q_full(b), filled);
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         const int nst = is_k ? kKS : kVS;
         const int32_t oob = (int32_t)(a.num_blocks * bs);  // a row past the cache: zero fill
         const uint32_t q_bytes = 2u * (uint32_t)q_rows * 128u;
-        auto full_of = [&](int st) { return is_k ? k_full(st) : (F8 ? vc_full(st) : v_full(st)); };
+        auto full_of = [&](int st) { return is_k ? k_full(st) : v_full(st); };
         // cursor over the stream: tile j of item w of pair q
         PairItem i0 = item_at(0), i1 = item_at(1);
         int32_t q = 0, j = 0;
@@ -364,11 +371,9 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 const bool good = id >= 0 && id < a.num_blocks;
                 if (!good && is_k) report_status(a.status, PCP_ERR_RANGE);
                 const int32_t y = good ? id * bs : oob;
-                const uint32_t dst = sbase + (is_k ? C::kK + st * C::kKTileBytes : C::kV + st * C::kTileBytes);
-                if constexpr (F8) {
-                    // K: the codes, 128-byte swizzled, as the e4m3 operand; V: the codes
-                    // where half 1 of the f16 tile goes, unswizzled, for the converters
-                    tma_load_3d(dst + (is_k ? 0 : C::kHalfBytes) + lane * bs * kD, tm, fb, 0, hk, y);
+                const uint32_t dst = sbase + (is_k ? C::kK : C::kV) + st * C::kTileBytes;
+                if constexpr (F8) {  // the codes, 128-byte swizzled, as the e4m3 operands
+                    tma_load_3d(dst + lane * bs * kD, tm, fb, 0, hk, y);
                 } else {
                     for (int h = 0; h < 2; ++h)
                         tma_load_3d(dst + h * C::kHalfBytes + lane * bs * 128, tm, fb, h * 64, hk, y);
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         // the stream's order. They share no operand, and each commit covers the MMAs of
         // the thread that makes it, so the two need no ordering between them.
         if (lane == 0) {
-            auto k_desc = [&](int s) { return sdesc_sw128(sbase + C::kK + s * C::kKTileBytes, 16, 1024); };
+            auto k_desc = [&](int s) { return sdesc_sw128(sbase + C::kK + s * C::kTileBytes, 16, 1024); };
             auto v_desc = [&](int s) {
                 return sdesc_sw128(sbase + C::kV + s * C::kTileBytes, C::kHalfBytes, 1024);
             };
@@ -451,11 +456,19 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                             if (!(ok = mbar_wait(o_free(w), (c[w] & 1) ^ 1, abort_flag))) break;
                             tc_fence_after();
                             const uint64_t vd = v_desc(g % kVS), pd = p_desc(w);
+                            const uint32_t to = tmem + C::kTmemO + w * kNO;
+                            if constexpr (F8) {  // 32 keys (rows of 128 bytes of V, 32 bytes of P^T's) per MMA
 #pragma unroll
-                            for (int ks = 0; ks < kKeys / 16; ++ks) {
-                                const uint32_t poff = ((ks / 4) * (kNO * 128) + (ks % 4) * 32) >> 4;
-                                mma_ss(tmem + C::kTmemO + w * kNO, vd + (uint32_t)(ks * 2048 >> 4), pd + poff,
-                                       C::kIdescO, ks > 0 ? 1u : 0u);
+                                for (int ks = 0; ks < kKeys / 32; ++ks)
+                                    mma_ss_e4m3(to, vd + (uint32_t)(ks * 4096 >> 4), pd + (uint32_t)(ks * 2), C::kIdescO,
+                                                ks > 0 ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int ks = 0; ks < kKeys / 16; ++ks) {
+                                    const uint32_t poff = ((ks / 4) * (kNO * 128) + (ks % 4) * 32) >> 4;
+                                    mma_ss(to, vd + (uint32_t)(ks * 2048 >> 4), pd + poff, C::kIdescO,
+                                           ks > 0 ? 1u : 0u);
+                                }
                             }
                             mma_commit(o_full(w));
                             mma_commit(v_empty(g % kVS));
@@ -468,47 +481,24 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
             if (!ok) report_status(a.status, PCP_ERR_TIMEOUT);
         }
     } else if (F8 && warp >= kConvWarp0) {
-        // ---------------------------------------------------------------- FP8 converters
-        // Set 0 (warps 12-15) also turns each item's q into its e4m3 terms; the stream's V
-        // tiles are widened by set g % (number of sets).
-        constexpr int kSets = F8 ? conv_warps(F8, GP) / 4 : 1;
-        const int cset = (warp - kConvWarp0) / 4, cw = (warp - kConvWarp0) % 4;
-        const int ct = (threadIdx.x - kConvWarp0 * 32) % kConvThreads;
-        uint32_t g = 0;
+        // ---------------------------------------------------------------- e4m3: q terms
+        const int cw = warp - kConvWarp0;
         bool ok = true;
         for (int32_t q = 0; ok && item_of_round(2 * q) < total; ++q) {
-            const PairItem it[2] = {item_at(2 * q),
-                                    item_at(2 * q + 1)};
-            const int32_t most = max(it[0].nt, it[1].nt);
-            for (int j = 0; j < most && ok; ++j) {
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (j >= it[w].nt || !ok) continue;
-                    if (j == 0 && cset == 0) {
-                        const int qb = q_buf(q, w);
-                        if (!(ok = mbar_wait_warp(qc_full(qb), q_use(q), abort_flag))) break;
-                        if (q_to_e4m3_terms<GP>(smem + C::kQ + qb * C::kQBytes, smem + C::kQC + qb * C::kQCBytes,
-                                                reinterpret_cast<float*>(smem + C::kQs) + qs_slot(q, w) * kGS, cw, lane, G) &&
-                            lane == 0)
-                            report_status(a.status, PCP_ERR_RANGE);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(q_full(qb));
-                            mbar_arrive(q_ready(qs_slot(q, w)));
-                        }
-                    }
-                    if ((int)(g % kSets) == cset) {
-                        const int vs = g % kVS;
-                        const int32_t v0 = it[w].lo + j * kKeys;
-                        if (!(ok = mbar_wait_warp(vc_full(vs), (g / kVS) & 1, abort_flag))) break;
-                        widen_tile(smem + C::kV + vs * C::kTileBytes, min(kKeys, it[w].hi - v0), ct,
-                                   [&](int r) { return it[w].live(v0 + r); });
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(v_full(vs));
-                    }
-                    ++g;
+            for (int w = 0; w < 2; ++w) {
+                if (item_of_round(2 * q + w) >= total) continue;
+                const int qb = q_buf(q, w);
+                if (!(ok = mbar_wait_warp(qc_full(qb), q_use(q), abort_flag))) break;
+                if (q_to_e4m3_terms<GP>(smem + C::kQ + qb * C::kQBytes, smem + C::kQC + qb * C::kQCBytes,
+                                        reinterpret_cast<float*>(smem + C::kQs) + qs_slot(q, w) * kGS, cw, lane, G) &&
+                    lane == 0)
+                    report_status(a.status, PCP_ERR_RANGE);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(q_full(qb));
+                    mbar_arrive(q_ready(qs_slot(q, w)));
                 }
             }
         }
@@ -525,9 +515,10 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
         float* red_m = reinterpret_cast<float*>(smem + C::kRed) + wg * 2 * 4 * kGS;
         float* red_l = reinterpret_cast<float*>(smem + C::kSum) + wg * 2 * 4 * kGS;
         uint8_t* pbuf = smem + C::kP + wg * C::kPBytes;
-        // this key's column of P^T: chunk (t % 64) / 8 of each row, swizzled by the row
-        uint8_t* pcol = pbuf + (t >> 6) * (kNO * 128) + (t & 7) * 2;
-        const int chunk = (t & 63) >> 3;
+        // this key's column of P^T: bf16: chunk (t % 64) / 8 of each row of half t / 64; e4m3:
+        // chunk t / 16 of each row; swizzled by the row
+        uint8_t* pcol = F8 ? pbuf + (t & 15) : pbuf + (t >> 6) * (kNO * 128) + (t & 7) * 2;
+        const int chunk = F8 ? t >> 4 : (t & 63) >> 3;
         uint32_t gt = 0, c = 0;  // tiles of the stream before this pair, and this warpgroup's
         bool ok = true;     // every wait of this thread so far completed
         bool stop = false;  // the warpgroup's joint decision to stop, once per item
@@ -570,8 +561,13 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_free(wg));
 #pragma unroll
-                for (int h = 0; h < GP; ++h)
-                    acc[h] = acc[h] * alpha[h] + (__uint_as_float(o[h]) + __uint_as_float(o[kGS + h]));
+                for (int h = 0; h < GP; ++h) {
+                    const float o0 = __uint_as_float(o[h]), o1 = __uint_as_float(o[kTS + h]);
+                    if constexpr (F8)  // the terms' powers of two taken back
+                        acc[h] = acc[h] * alpha[h] + (o0 * 0x1p-8f + (o1 * 0x1p-12f + __uint_as_float(o[2 * kTS + h]) * 0x1p-16f));
+                    else
+                        acc[h] = acc[h] * alpha[h] + (o0 + o1);
+                }
             };
             for (int j = 0; j < it.nt; ++j, ++c) {
                 const int32_t v0 = it.lo + j * kKeys;
@@ -607,22 +603,38 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                     const float pe = fast_exp2(x[h] - m_new);
                     l_t[h] = l_t[h] * alpha + pe;
                     a_prev[h] = alpha;
-                    const uint16_t hi = to16<F8>(pe);
-                    const uint16_t lo = to16<F8>(pe - from16<F8>(hi));
-                    *reinterpret_cast<uint16_t*>(pcol + h * 128 + ((chunk ^ (h & 7)) << 4)) = hi;
-                    *reinterpret_cast<uint16_t*>(pcol + (kGS + h) * 128 + ((chunk ^ (h & 7)) << 4)) = lo;
+                    if constexpr (F8) {
+                        float rem = pe;
+#pragma unroll
+                        for (int n = 0; n < 3; ++n) {
+                            const float up = n == 0 ? 0x1p8f : n == 1 ? 0x1p12f : 0x1p16f;
+                            const uint32_t code = f32x2_to_e4m3x2(rem * up, 0.f);
+                            const int row = n * kTS + h;
+                            pcol[row * 128 + ((chunk ^ (row & 7)) << 4)] = (uint8_t)code;
+                            if (n < 2) {
+                                float back[4];
+                                e4m3x4_to_f32(code, back);
+                                rem -= back[0] * (1.f / up);  // exact: both hold few significant bits
+                            }
+                        }
+                    } else {
+                        const uint16_t hi = to16<F8>(pe);
+                        const uint16_t lo = to16<F8>(pe - from16<F8>(hi));
+                        *reinterpret_cast<uint16_t*>(pcol + h * 128 + ((chunk ^ (h & 7)) << 4)) = hi;
+                        *reinterpret_cast<uint16_t*>(pcol + (kTS + h) * 128 + ((chunk ^ (h & 7)) << 4)) = lo;
+                    }
                 }
                 // keys that the row does not see: zero their V rows (cache rows before the window,
                 // unwritten slots of the last page, stale rows after it) once the tile has landed
                 const bool gaps = nvalid < kKeys || (v0 < it.gap_end && it.gap_end > it.sinks);
-                if (!F8 && gaps) {
+                if (gaps) {
                     const uint32_t both = min(it.nt, n_other);  // tiles at which the stream alternates
                     const uint32_t g = gt + (j < (int)both ? 2 * j + wg : both + j), vs = g % kVS;
                     ok &= mbar_wait_warp(v_full(vs), (g / kVS) & 1, abort_flag);
                     if (!valid) {
                         uint8_t* vrow = smem + C::kV + vs * C::kTileBytes + t * 128;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int h = 0; h < (F8 ? 1 : 2); ++h)
 #pragma unroll
                             for (int c2 = 0; c2 < 8; ++c2)
                                 *reinterpret_cast<uint4*>(vrow + h * C::kHalfBytes + ((c2 ^ (t & 7)) << 4)) =
@@ -677,9 +689,9 @@ int launch_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t ma
     const int q_rows = a.hq < kN ? a.hq : kN;
     CUtensorMap tq, tk, tv;
     bool maps = make_box_map(&tq, a.q, kD, 2, a.hq, a.total_q, 64, q_rows, 1, true);
-    if (F8)  // K codes 128-byte swizzled (the MMA operand), V codes plain (for the converters)
+    if (F8)
         maps = maps && make_box_map(&tk, a.key_cache, kD, 1, a.hkv, slots, kD, 1, a.block_size, true) &&
-               make_box_map(&tv, a.value_cache, kD, 1, a.hkv, slots, kD, 1, a.block_size, false);
+               make_box_map(&tv, a.value_cache, kD, 1, a.hkv, slots, kD, 1, a.block_size, true);
     else
         maps = maps && make_box_map(&tk, a.key_cache, kD, 2, a.hkv, slots, 64, 1, a.block_size, true) &&
                make_box_map(&tv, a.value_cache, kD, 2, a.hkv, slots, 64, 1, a.block_size, true);
@@ -689,11 +701,11 @@ int launch_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t ma
         cudaFuncSetAttribute(decode_pair_kernel<F8, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) {
         if (a.inline_items) {  // nothing of this call to be chained behind
-            decode_pair_kernel<F8, GP><<<a.num_sms, tc_threads(F8, GP), smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
+            decode_pair_kernel<F8, GP><<<a.num_sms, PairCfg<F8, GP>::kThreads, smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
                                                                                       max_splits, q_rows);
             e = cudaGetLastError();
         } else {
-            e = launch_chained(decode_pair_kernel<F8, GP>, dim3(a.num_sms), dim3(tc_threads(F8, GP)), smem, stream, tq,
+            e = launch_chained(decode_pair_kernel<F8, GP>, dim3(a.num_sms), dim3(PairCfg<F8, GP>::kThreads), smem, stream, tq,
                                tk, tv, a, dec_out, dec_lse, max_splits, q_rows);
         }
     }

@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(tc_threads(F8, GP), 1)
                 const int vs = g % kVS;
                 const int nvalid = min(kKeys, it.hi - it.lo - j * kKeys);
                 if (!(ok = mbar_wait_warp(vc_full(vs), (g / kVS) & 1, abort_flag))) break;
-                widen_tile(smem + C::kV + vs * C::kTileBytes, nvalid, ct, [](int) { return true; });
+                widen_tile(smem + C::kV + vs * C::kTileBytes, nvalid, ct);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(v_full(vs));

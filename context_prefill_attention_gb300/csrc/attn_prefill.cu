@@ -194,8 +194,8 @@ __device__ __forceinline__ Item decode_item(const Unit* units, int32_t idx, int3
 // What bounds the packed kernel: per item of two tiles about 4 us in which the tensor
 // pipe waits (the last tile's softmax, O's way out, the first tile's), 3 us for edges and
 // stores, and 1.7 us per 128-key tile, the pace of the issuing thread (as in the
-// plain form). Measured with 8 x 8192 tokens, 32 q / 8 kv heads, D = 128: window 64 6.9 us
-// per item, 1024 20.4 us (937 TFLOP/s of visible pairs), 8192 62.5 us (1299).
+// plain form). Measured with 8 x 8192 tokens, 32 q / 8 kv heads, D = 128: window 64 6.3 us
+// per item, 1024 20.2 us (948 TFLOP/s of visible pairs), 8192 62.4 us (1308).
 __device__ __forceinline__ PackedUnit packed_unit(const PrefillArgs& a, int32_t req, int32_t q_start, int32_t q_len,
                                                   int32_t first_pos, int32_t mt, int32_t span, int32_t k_lo,
                                                   int32_t k_hi, int32_t pass) {
@@ -1542,15 +1542,15 @@ __global__ void __launch_bounds__(NT, 1)
     }
     // The SMs of the decode rows and the prefixes' shards: lane n - 1 of warp 0 models n
     // shards. Times measured on GB300 (us): a decode item 1 and a 128-key tile 0.95
-    // (FP8 1.15) of an SM's time where few SMs draw on HBM, a tile (64 KB; FP8 32 KB)
-    // 1 / 95 (1 / 150) of the GPU's; a packed item 4.5 and a tile 1.75 (FP8 5.5, 1.95)
+    // (FP8 0.8) of an SM's time where few SMs draw on HBM, a tile (64 KB; FP8 32 KB)
+    // 1 / 95 (1 / 175) of the GPU's; a packed item 4.5 and a tile 1.75 (FP8 5.5, 1.95)
     // of an SM's; a partial to merge total_q x hq x d x 8 bytes at 10 TB/s. Side by
     // side, both kernels run about 6 % longer than alone.
     __syncthreads();
     if (warp == 0) {
         const bool f8 = a.k_descale != nullptr;
-        const float dec_us = (float)a.hkv * (1.0f * cost[0] + (f8 ? 1.15f : 0.95f) * cost[1]);
-        const float dec_all = 6.f + (float)a.hkv * cost[1] / (f8 ? 150.f : 95.f);
+        const float dec_us = (float)a.hkv * (1.0f * cost[0] + (f8 ? 0.8f : 0.95f) * cost[1]);
+        const float dec_all = 6.f + (float)a.hkv * cost[1] / (f8 ? 175.f : 95.f);
         const float item_us = f8 ? 5.5f : 4.5f, tile_us = f8 ? 1.95f : 1.75f;
         const float merge_us = (float)a.total_q * a.hq * a.d * 8e-7f;
         const int32_t nsm = a.num_sms, most = min(32, max(1, a.nparts - 1));

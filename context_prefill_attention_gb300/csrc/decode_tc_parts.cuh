@@ -88,9 +88,7 @@ __device__ __forceinline__ float warp_scatter(const float (&x)[GP], int lane) {
 // goes; the eight threads of a row are in one warp and all load before any of
 // them stores. Rows at or past nvalid are written as zeros (their codes may be
 // stale or unwritten cache slots). Run by the 128 converter threads.
-// live(r): further rows for which it is false are written as zeros too.
-template <typename Live>
-__device__ __forceinline__ void widen_tile(uint8_t* tile, int nvalid, int ct, Live live) {
+__device__ __forceinline__ void widen_tile(uint8_t* tile, int nvalid, int ct) {
     constexpr int kHalf = kKeys * 128;
     constexpr int kRpp = kConvThreads / 8;  // rows per pass
     constexpr int kBatch = 4;
@@ -106,7 +104,7 @@ __device__ __forceinline__ void widen_tile(uint8_t* tile, int nvalid, int ct, Li
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int r = r0 + kRpp * b + rsub;
-            c[b] = r < nvalid && live(r) ? *reinterpret_cast<const uint4*>(codes + r * kD + 16 * t)
+            c[b] = r < nvalid ? *reinterpret_cast<const uint4*>(codes + r * kD + 16 * t)
                                          : make_uint4(0, 0, 0, 0);
         }
         __syncwarp();

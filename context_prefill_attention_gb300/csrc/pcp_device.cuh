@@ -198,9 +198,11 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
            | ((uint32_t)(M >> 4) << 24);             // M / 16
 }
 
-// Instruction descriptor of kind::f8f6f4 with e4m3 A and B, fp32 D, both K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+// Instruction descriptor of kind::f8f6f4 with e4m3 A and B, fp32 D, B K-major;
+// a_mn selects the MN-major layout of A.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn = false) {
     return (1u << 4)                     // D format: f32; A and B format 0: e4m3
+           | ((a_mn ? 1u : 0u) << 15)
            | ((uint32_t)(N >> 3) << 17)  // N / 8
            | ((uint32_t)(M >> 4) << 24);  // M / 16
 }

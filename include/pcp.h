@@ -369,7 +369,10 @@ int pcp_attn_varlen_fp8kv(const void* q, const void* key_cache, const void* valu
  * tokens too; calls that may overlap on the GPU need one each. Errors: PCP_ERR_ARG also for window < 1 or
  * num_sinks < 0.
  * pcp_attn_window_fp8kv: the same over an FP8 (e4m3) cache, with the descales
- * and numerics of pcp_attn_varlen_fp8kv.
+ * and numerics of pcp_attn_varlen_fp8kv, except that one-token rows (head_dim 128,
+ * up to 8 q heads per kv head, at most 1024 rows) take the V codes as e4m3 operands
+ * too, against softmax weights carried as three e4m3 terms (12 significant bits,
+ * 2^-26 of the row's largest weight below).
  */
 size_t pcp_attn_window_workspace_size(int32_t num_rows, int32_t total_q, int32_t num_q_heads,
                                       int32_t num_kv_heads, int32_t head_dim, int32_t max_kv_len,

@@ -12,6 +12,8 @@ the LSE, held to the 1e-3 that pcp_attn_varlen is held to. An f16 weight (e4m3
 cache) is a multiple of 2^-24 below 2^-14, so it is off by up to 2^-25 there, with
 the largest weight of its row 1 or more and the sum p at least that: 2^-25 sum |v|
 over the visible keys besides (it shows where the weights that matter meet v = 0).
+One-token rows over an e4m3 cache carry P as three e4m3 terms, 2^-13 relative and 2^-26 of the
+largest weight: inside both.
 """
 import math
 
