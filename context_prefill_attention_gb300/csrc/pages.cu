@@ -15,7 +15,7 @@
 // steps of a call up to the page copies run in one cluster of kCluster blocks, a
 // cluster barrier between them, in place of a kernel each. Measured per call of a
 // stream of them: fork and release of four beams over 2000 pages 23.8 -> 20.6 us,
-// release and compaction of six requests over 600 pages 31 -> 23.7 us; but over
+// release and compaction of six requests over 600 pages 31 -> 20.9 us; but over
 // 36000 pages and 65000 entries, where eight blocks are too few, 55 -> 65 us.
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -2,7 +2,7 @@
 // window with sinks (pcp_attn_window) and a batch that shares prefixes
 // (pcp_attn_shared_prefix). Argument checks, workspace layout and the launch
 // sequence; the kernels are in attn_prefill.cu (packed tiles of tokens x q
-// heads), attn_decode_tc.cu and attn_decode.cu (one-token rows, the merge).
+// heads), attn_decode_pair.cu and attn_decode.cu (one-token rows, the merge).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -428,7 +428,8 @@ int pcp_build_prefix_groups(const pcp_row_t* rows, int32_t num_rows, const int32
  * in [0, 1024] (else PCP_ERR_ARG); with 0, prefixes may be NULL.
  * A row of one token takes the decode path whatever its is_decode.
  * With num_prefixes == 0 a call with num_rows >= total_q takes one-token rows
- * only (see pcp_attn_window). FP8 cache: the descales of a prefix are those of its req.
+ * only (see pcp_attn_window). FP8 cache: the descales of a prefix are those of its req
+ * (requests that share pages share descales); numerics of pcp_attn_window_fp8kv.
  * Every other argument, limit, check and error is that of pcp_attn_varlen; there
  * are no flags. workspace: at least pcp_attn_shared_prefix_workspace_size(
  * num_rows, num_prefixes, total_q, Hq, Hkv, D, max_blocks_per_req * block_size)
