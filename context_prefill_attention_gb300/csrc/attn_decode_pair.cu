@@ -33,6 +33,10 @@
 // a few one-token rows whose items all fit the SMs at once (a.inline_items) has no
 // scheduler: one warp of each CTA reads the rows (kInlineRows at most) and finds
 // the CTA's two items itself. Measured, 4 rows with a window of 1024: 18.5 -> 16.4 us.
+// Nor has it a merge where a cluster can take each row and kv head (a.cluster): its
+// blocks have two splits each and join them through each other's shared memory; the
+// call is this one kernel. 4 rows 16.4 -> 14.4 us, 1 row 14.4 -> 10.5, 8 rows with a
+// window of 16384 95 -> 85 us.
 //
 // What bounds it: HBM with a bf16 cache where the rows fill the SMs (56 rows of 1060
 // slots: 242 MB in 46 us, 5.3 TB/s; 128 of 4132 over an e4m3 cache: 1.04 GB in 182 us,
@@ -129,6 +133,7 @@ static_assert(sizeof(PairItem) == 40, "two of them fit at PairCfg::kOwn");
 // all rows, splits and kv heads (row by row, split by split, head by head); returns
 // the item count. CTA 0 also reports bad rows and writes the merge records.
 constexpr int kInlineRows = 64;
+constexpr int kMaxCluster = 8;  // blocks of a cluster at most (a.cluster)
 __device__ __forceinline__ int32_t inline_items(const PrefillArgs& a, int32_t p0, int32_t p1, PairItem* own,
                                                 int lane) {
     constexpr int kPer = kInlineRows / 32;
@@ -193,6 +198,38 @@ __device__ __forceinline__ int32_t inline_items(const PrefillArgs& a, int32_t p0
             }
     }
     return total;
+}
+
+// a.cluster: one warp's work of finding the block's two items, splits 2 x rank and 2 x
+// rank + 1 of the cluster's row and kv head; returns how many of them there are, and in
+// *splits those of the cluster.
+__device__ __forceinline__ int32_t cluster_items(const PrefillArgs& a, PairItem* own, int32_t* splits, int lane) {
+    const int32_t unit = (int32_t)blockIdx.x / a.cluster, rank = (int32_t)blockIdx.x - unit * a.cluster;
+    const int32_t ri = unit / a.hkv;
+    pcp_row_t row = a.rows[ri];
+    const bool ok = row_in_range(row, a.num_reqs, a.total_q, (int64_t)a.max_blocks * a.block_size) && row.q_len == 1;
+    if (!ok) row.kv_end = 0;
+    const KeyRange kr = key_range(a, row, 0);
+    PairItem it{};
+    it.row = ri;
+    it.req = row.req;
+    it.q_start = row.q_start;
+    it.hk = unit - ri * a.hkv;
+    it.sinks = kr.sinks;
+    it.gap_end = kr.lo - kr.shift;
+    it.shift = kr.shift;
+    if (!ok && rank == 0 && it.hk == 0 && lane == 0) report_status(a.status, PCP_ERR_RANGE);
+    int32_t n = 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        it.lo = (2 * rank + w) * a.chunk;
+        it.hi = min(kr.len, it.lo + a.chunk);
+        it.nt = it.hi > it.lo ? (it.hi - it.lo + kKeys - 1) / kKeys : 0;
+        n += it.nt > 0;
+        if (lane == 0) own[w] = it;
+    }
+    *splits = (kr.len + a.chunk - 1) / a.chunk;
+    return n;
 }
 
 template <bool F8, int GP>
@@ -267,11 +304,17 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
     }
     PairItem* own = reinterpret_cast<PairItem*>(smem + C::kOwn);
     int32_t* own_total = reinterpret_cast<int32_t*>(smem + C::kMisc + 8);
+    int32_t* row_splits = own_total + 1;  // a.cluster: splits of the cluster's row
     if (a.inline_items) {
         grid_launch_dependents();
         if (warp == 0) {
-            const int32_t n = inline_items(a, (int32_t)blockIdx.x, 2 * a.num_sms - 1 - (int32_t)blockIdx.x, own, lane);
-            if (lane == 0) *own_total = n;
+            int32_t n, splits = 0;
+            if (a.cluster) n = cluster_items(a, own, &splits, lane);
+            else n = inline_items(a, (int32_t)blockIdx.x, 2 * a.num_sms - 1 - (int32_t)blockIdx.x, own, lane);
+            if (lane == 0) {
+                *own_total = n;
+                *row_splits = splits;
+            }
         }
         __syncthreads();
     } else {
@@ -287,6 +330,7 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
     // (A CTA without items gets `total` in every round: the snake's backward rounds
     // would be negative for it.)
     auto item_of_round = [&](int32_t rd) -> int32_t {
+        if (a.cluster) return rd;  // `total` items, of rounds 0 and 1
         if ((int32_t)blockIdx.x >= step) return total;
         return rd * step + ((rd & 1) ? step - 1 - (int32_t)blockIdx.x : (int32_t)blockIdx.x);
     };
@@ -653,6 +697,18 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
             if (lane % kSpan == 0) rl[wq * kGS + hl] = wl;
             const float vd = F8 ? __ldg(a.v_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
             if ((stop = bar_wg_or(1 + wg, !ok))) break;
+            if (a.cluster) {  // the split's sums for the cluster's merge, where its maxima and P were
+                float* part = reinterpret_cast<float*>(pbuf);
+#pragma unroll
+                for (int h = 0; h < GP; ++h) {
+                    part[h * kD + t] = acc[h];
+                    if (t == 0) {
+                        red_m[h] = m_run[h];
+                        red_m[kGS + h] = rl[h] + rl[kGS + h] + rl[2 * kGS + h] + rl[3 * kGS + h];
+                    }
+                }
+                continue;
+            }
 #pragma unroll
             for (int h = 0; h < GP; ++h) {
                 if (h >= G) continue;
@@ -675,6 +731,46 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
     }
 
     __syncwarp();  // lane 0 of the MMA warps and of the producers worked alone: reconverge first
+    if (a.cluster) {
+        // the row's splits joined: head h by warpgroup h of the cluster (mod their number), a dim
+        // per thread, reading the sums of split s where warpgroup s % 2 of block s / 2 left them
+        cluster_sync();
+        const int32_t n = *row_splits;
+        if (warp < 8 && n > 0) {
+            const int wg = warp / 4, t = threadIdx.x % 128;
+            const PairItem it = own[0];
+            const float vd = F8 ? __ldg(a.v_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
+            const int32_t rank = (int32_t)blockIdx.x % a.cluster;
+            for (int h = 2 * rank + wg; h < G; h += 2 * a.cluster) {
+                float m[2 * kMaxCluster], l[2 * kMaxCluster], x[2 * kMaxCluster];
+#pragma unroll
+                for (int s = 0; s < 2 * kMaxCluster; ++s) {
+                    m[s] = -INFINITY;
+                    l[s] = x[s] = 0.f;
+                    if (s >= n) continue;
+                    const uint32_t at = sbase + C::kRed + (s & 1) * 2 * 4 * kGS * 4 + h * 4;
+                    m[s] = cluster_load(at, s >> 1);
+                    l[s] = cluster_load(at + kGS * 4, s >> 1);
+                    x[s] = cluster_load(sbase + C::kP + (s & 1) * C::kPBytes + (h * kD + t) * 4, s >> 1);
+                }
+                float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
+                for (int s = 0; s < 2 * kMaxCluster; ++s) M = fmaxf(M, m[s]);
+#pragma unroll
+                for (int s = 0; s < 2 * kMaxCluster; ++s) {
+                    const float f = s < n ? fast_exp2(m[s] - M) : 0.f;
+                    L += f * l[s];
+                    O += f * x[s];
+                }
+                const int32_t head = it.hk * G + h;
+                reinterpret_cast<__nv_bfloat16*>(a.out)[((size_t)it.q_start * a.hq + head) * kD + t] =
+                    __float2bfloat16_rn(L > 0.f ? O / L * vd : 0.f);
+                if (t == 0) a.lse[(size_t)head * a.total_q + it.q_start] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no block ends while another still reads its shared memory
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -700,7 +796,11 @@ int launch_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t ma
     cudaError_t e =
         cudaFuncSetAttribute(decode_pair_kernel<F8, GP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) {
-        if (a.inline_items) {  // nothing of this call to be chained behind
+        if (a.cluster) {
+            e = launch_clusters((unsigned)a.cluster, decode_pair_kernel<F8, GP>, dim3(a.num_rows * a.hkv * a.cluster),
+                                dim3(PairCfg<F8, GP>::kThreads), smem, stream, tq, tk, tv, a, dec_out, dec_lse, max_splits,
+                                q_rows);
+        } else if (a.inline_items) {  // nothing of this call to be chained behind
             decode_pair_kernel<F8, GP><<<a.num_sms, PairCfg<F8, GP>::kThreads, smem, stream>>>(tq, tk, tv, a, dec_out, dec_lse,
                                                                                       max_splits, q_rows);
             e = cudaGetLastError();
@@ -718,6 +818,28 @@ int launch_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t ma
 bool decode_inline_applies(const PrefillArgs& a, int32_t max_splits) {
     return decode_tc_applies(a) && a.num_prefixes == 0 && a.total_q <= a.num_rows && a.num_rows <= kInlineRows &&
            (int64_t)a.num_rows * a.hkv * max_splits <= 2 * a.num_sms;
+}
+
+// Blocks per row and kv head of a window call whose one-token rows (as many as tokens) a
+// cluster each can take side by side, and then in *chunk the keys per split; 0: none.
+// Clusters that all run at once: 15 of 8 blocks, 36 of 4, 76 of 2 fit the 152 SMs (one
+// more and 1024-key windows take 18.5 us instead of 11.1, 22.6 instead of 14.3), a few
+// are left for GPCs with fewer SMs. Where they leave SMs idle, their splits are at most one
+// tile longer than those that a call with a merge would have: a row of 16452 slots and
+// one kv head takes 27.4 us in one cluster, 22.6 with 304 splits and a merge (but 64
+// such pairs of a row and a head, two blocks each, 85 against 95). One split per
+// row (max_splits 1) needs no joining.
+int32_t decode_cluster(const PrefillArgs& a, int64_t max_len, int32_t max_splits, int32_t* chunk) {
+    if (!decode_tc_applies(a) || a.num_prefixes > 0 || a.total_q > a.num_rows || max_splits == 1) return 0;
+    const int64_t units = (int64_t)a.num_rows * a.hkv;
+    for (int32_t c = kMaxCluster; c >= 1; c /= 2) {
+        if ((units + 5) * c > a.num_sms) continue;
+        const int64_t keys = (max_len + 2 * c * kKeys - 1) / (2 * c * kKeys) * kKeys;
+        if (units * c * 4 < a.num_sms * 3 && keys > *chunk + kKeys) return 0;
+        *chunk = (int32_t)keys;
+        return c;
+    }
+    return 0;
 }
 
 int launch_decode_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,

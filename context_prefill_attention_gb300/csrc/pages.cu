@@ -66,11 +66,6 @@ PagesLayout pages_layout(int64_t num_blocks) {
     return w;
 }
 
-// A cluster barrier that also orders the blocks' global memory accesses.
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Sum of v over the block, to every thread.
 template <int kThreads = kPageThreads>
 __device__ __forceinline__ int32_t block_sum(int32_t v, int32_t* warp_sums) {

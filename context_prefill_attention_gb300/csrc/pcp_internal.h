@@ -134,6 +134,7 @@ struct PrefillArgs {
     int32_t num_sms;            // CTAs of the persistent kernels
     int32_t overlap;            // the decode kernel is the persistent one: it can share the SMs
     int32_t inline_items;       // the decode kernel finds its items itself (decode_inline_applies)
+    int32_t cluster;            // ... for a cluster of this many blocks per row and kv head (0: for the whole grid)
     MergeTask* merge;           // ... and writes the merge records
     int32_t direct;             // decode rows have one partial each: written straight to out and lse
     int32_t slots;              // token tiles per packed item: 1 or 2
@@ -145,6 +146,20 @@ struct PrefillArgs {
 };
 
 #ifdef __CUDACC__
+// Launch with one attribute.
+template <typename... Params, typename... Args>
+cudaError_t launch_attr(cudaLaunchAttribute attr, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                        cudaStream_t stream, Args&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // Launch a kernel that may start while the one before it on the stream still
 // runs (it calls grid_wait before it touches that one's results): hides the
 // launch and the block's set-up behind the predecessor's end.
@@ -154,14 +169,19 @@ cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, siz
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+    return launch_attr(attr, kernel, grid, block, smem, stream, static_cast<Args&&>(args)...);
+}
+
+// A grid of clusters of `size` consecutive blocks.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(unsigned size, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t stream, Args&&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    return launch_attr(attr, kernel, grid, block, smem, stream, static_cast<Args&&>(args)...);
 }
 
 // The keys of a one-token row in a window or shared-prefix call, walked as whole
@@ -253,6 +273,8 @@ int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, in
 // Whether a window call's rows are one-token rows (as many as tokens) few enough for
 // the decode kernel to find its items without the scheduler.
 bool decode_inline_applies(const PrefillArgs& a, int32_t max_splits);
+// Whether a cluster per row and kv head takes them: its blocks (0: no), and their keys per split.
+int32_t decode_cluster(const PrefillArgs& a, int64_t max_len, int32_t max_splits, int32_t* chunk);
 int launch_decode_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                        cudaStream_t stream);
 int launch_range_merge(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out, const float* dec_lse,

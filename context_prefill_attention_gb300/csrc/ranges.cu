@@ -227,7 +227,8 @@ int range_call(const RangeCall& c) {
     a.direct = !shared && w.max_splits == 1;
     MergeTask* tasks = reinterpret_cast<MergeTask*>(ws + w.merge);
     a.merge = tasks;
-    a.inline_items = decode_inline_applies(a, w.max_splits);
+    a.cluster = decode_cluster(a, max_len, w.max_splits, &a.chunk);
+    a.inline_items = a.cluster > 0 || decode_inline_applies(a, w.max_splits);
     int rc = PCP_OK;
     if (!a.inline_items)
         rc = launch_range_schedule(a, reinterpret_cast<PackedUnit*>(ws + w.units),
@@ -245,7 +246,7 @@ int range_call(const RangeCall& c) {
         rc = launch_packed(a, c.stream);
         if (rc != PCP_OK) return rc;
     }
-    if (a.direct) return PCP_OK;
+    if (a.direct || a.cluster > 0) return PCP_OK;
     return launch_range_merge(a, tasks, dec_out, dec_lse, w.max_splits, c.stream);
 }
 

@@ -49,6 +49,42 @@ def test_long_decode_and_prefill_with_many_sinks():
     b.check(*b.run())
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rows,hq,hkv", [(1, 4, 1), (14, 8, 1), (15, 8, 1), (2, 8, 8), (33, 3, 1), (9, 32, 8), (18, 16, 8), (19, 8, 8),
+                                         (1, 16, 1), (40, 32, 2)])
+def test_few_rows_of_all_lengths(rows, hq, hkv, fp8):
+    """Up to 152 pairs of a row and a kv head, whose splits a cluster of 8, 4, 2 or 1 blocks joins: rows
+    of one key, of fewer splits than the others, of whole tiles; windows that need no split, and long ones."""
+    if fp8 and hq // hkv > 8:
+        pytest.skip("16 q heads per kv head over an e4m3 cache take the CUDA-core kernel")
+    ctx = [(0, 3, 127, 128, 700, 1500, 1600, 4000)[(3 * i + rows) % 8] for i in range(rows)]
+    for window, sinks in ((64, 0), (1500, 4), (900, 200), (5000, 0)):
+        b = Batch([(1, c) for c in ctx], hq, hkv, 128, 16, window=window, sinks=sinks, seed=rows, fp8=fp8)
+        out, lse = b.run()
+        b.check(out, lse)
+        again, again_lse = b.run()
+        assert torch.equal(out, again) and torch.equal(lse, again_lse)
+
+
+def test_bad_rows_among_few():
+    P = _pcp()
+    b = Batch([(1, 900), (1, 2000), (1, 0), (1, 1100)], 8, 2, 128, 16, window=1000, sinks=4, seed=2)
+    want, want_lse = b.run()
+    for col, x in ((0, 4), (3, 0), (3, 2), (5, 10 ** 6), (2, 4)):
+        old = b.rows_dev[1, col].clone()
+        b.rows_dev[1, col] = x
+        out, lse = b.run()
+        torch.cuda.synchronize()
+        assert int(b.status.item()) == P.PCP_ERR_RANGE
+        for t in (0, 2, 3):
+            assert torch.equal(out[t], want[t]) and torch.equal(lse[:, t], want_lse[:, t])
+        assert (out[1] == 7.0).all() and (lse[:, 1] == 7.0).all()
+        b.rows_dev[1, col] = old
+        b.status.zero_()
+    out, lse = b.run()
+    b.check(out, lse)
+
+
 def test_many_decode_rows():
     """More rows than the tensor-core decode takes."""
     b = Batch([(1, (37 * i) % 400) for i in range(1100)], 4, 2, 128, 16, window=64, sinks=2, seed=5)
