@@ -36,7 +36,7 @@
 // Nor has it a merge where a cluster can take each row and kv head (a.cluster): its
 // blocks have two splits each and join them through each other's shared memory; the
 // call is this one kernel. 4 rows 16.4 -> 14.4 us, 1 row 14.4 -> 10.5, 8 rows with a
-// window of 16384 95 -> 85 us.
+// window of 16384 95 -> 85 us; 8 rows behind 1008 shared keys 25.3 -> 16.4 (see decode_cluster).
 //
 // What bounds it: HBM with a bf16 cache where the rows fill the SMs (56 rows of 1060
 // slots: 242 MB in 46 us, 5.3 TB/s; 128 of 4132 over an e4m3 cache: 1.04 GB in 182 us,
@@ -88,7 +88,7 @@ struct PairCfg {
     static constexpr int kThreads = 32 * (F8 ? 16 : 12);  // e4m3: four warps turn q into its terms
     static constexpr int kMisc = kBar + kNumBars * 8;  // TMEM address, abort flag, item count
     static constexpr int kOwn = kMisc + 16;            // PairItem [2]: a.inline_items
-    static constexpr int kSmem = kOwn + 2 * 40 + 1024;  // + alignment slack
+    static constexpr int kSmem = kOwn + 2 * 44 + 1024;  // + alignment slack
     static constexpr uint32_t kTmemS = 0, kTmemO = 2 * kNS;
     static constexpr uint32_t kTmemCols = 2 * kNS + 2 * kNO <= 64 ? 64 : 128;
     static constexpr uint32_t kIdescS = F8 ? idesc_e4m3(128, kNS) : idesc_bf16(128, kN, false, false);
@@ -104,6 +104,7 @@ static_assert(PairCfg<true, 4>::kQC % 1024 == 0 && PairCfg<true, 4>::kP % 1024 =
 struct PairItem {
     int32_t row, req, q_start, hk, lo, hi, nt;  // slots [lo, hi) of the row's walk, in nt tiles
     int32_t sinks, gap_end, shift;
+    int32_t preq;  // request whose table names the pages of the sinks (a.cluster: or of the shared prefix)
     // whether slot v holds a key that the row sees
     __device__ __forceinline__ bool live(int32_t v) const { return v < sinks || v >= gap_end; }
 };
@@ -123,17 +124,19 @@ __device__ __forceinline__ PairItem pair_item(const PrefillArgs& a, int32_t p, i
     it.sinks = y.y;
     it.gap_end = y.z;
     it.shift = y.w;
+    it.preq = it.req;
     it.nt = (it.hi - it.lo + kKeys - 1) / kKeys;
     return it;
 }
 
-static_assert(sizeof(PairItem) == 40, "two of them fit at PairCfg::kOwn");
+static_assert(sizeof(PairItem) == 44, "two of them fit at PairCfg::kOwn");
 
 // a.inline_items: one warp's work of finding the items `p0` and `p1` (-1: none) among
 // all rows, splits and kv heads (row by row, split by split, head by head); returns
 // the item count. CTA 0 also reports bad rows and writes the merge records.
 constexpr int kInlineRows = 64;
 constexpr int kMaxCluster = 8;  // blocks of a cluster at most (a.cluster)
+constexpr int kPrefixKeys = 1024;  // keys of a split at most where rows read a shared prefix each
 __device__ __forceinline__ int32_t inline_items(const PrefillArgs& a, int32_t p0, int32_t p1, PairItem* own,
                                                 int lane) {
     constexpr int kPer = kInlineRows / 32;
@@ -185,7 +188,7 @@ __device__ __forceinline__ int32_t inline_items(const PrefillArgs& a, int32_t p0
             if (n >= before[k] && n < before[k] + splits[k]) {
                 PairItem it;
                 it.row = lane * kPer + k;
-                it.req = row[k].req;
+                it.req = it.preq = row[k].req;
                 it.q_start = row[k].q_start;
                 it.hk = p - n * a.hkv;
                 it.lo = (n - before[k]) * a.chunk;
@@ -202,33 +205,70 @@ __device__ __forceinline__ int32_t inline_items(const PrefillArgs& a, int32_t p0
 
 // a.cluster: one warp's work of finding the block's two items, splits 2 x rank and 2 x
 // rank + 1 of the cluster's row and kv head; returns how many of them there are, and in
-// *splits those of the cluster.
+// *splits those of the cluster. The splits are as even as whole tiles allow. A shared
+// prefix is walked as sinks are, its pages those of the group's request; a row begins at
+// or past its prefix, so its own pages follow, the first one again where the prefix ends
+// inside a page.
+constexpr int kClusterGroups = 16;  // prefix groups at most (every block checks them)
 __device__ __forceinline__ int32_t cluster_items(const PrefillArgs& a, PairItem* own, int32_t* splits, int lane) {
     const int32_t unit = (int32_t)blockIdx.x / a.cluster, rank = (int32_t)blockIdx.x - unit * a.cluster;
-    const int32_t ri = unit / a.hkv;
+    const int32_t ri = unit / a.hkv, ng = a.num_prefixes;
+    const int64_t max_kv = (int64_t)a.max_blocks * a.block_size;
+    pcp_prefix_t p{};
+    if (lane < ng) p = a.prefixes[lane];
     pcp_row_t row = a.rows[ri];
-    const bool ok = row_in_range(row, a.num_reqs, a.total_q, (int64_t)a.max_blocks * a.block_size) && row.q_len == 1;
+    bool ok = row_in_range(row, a.num_reqs, a.total_q, max_kv) && row.q_len == 1;
+    int32_t prefix = 0, preq = row.req;
+    if (ng > 0) {
+        // the group of this lane: fields in range, and its tokens after those of every earlier group
+        bool good = p.q_start >= 0 && p.q_len >= 1 && (int64_t)p.q_start + p.q_len <= a.total_q && p.req >= 0 &&
+                    p.req < a.num_reqs && p.prefix_len >= 1 && p.prefix_len <= max_kv;
+        const int64_t p1 = (int64_t)p.q_start + p.q_len;
+        for (int e = 0; e + 1 < ng; ++e) {
+            const int64_t end = __shfl_sync(0xffffffffu, p1, e);
+            if (lane > e) good = good && p.q_start >= end;
+        }
+        if (blockIdx.x == 0 && lane < ng && !good) report_status(a.status, PCP_ERR_RANGE);
+        // the row's group, which has to be good and to end where the row begins or before
+        const bool mine = lane < ng && row.q_start >= p.q_start && row.q_start < p1;
+        ok = ok && __all_sync(0xffffffffu, !mine || (good && row.kv_end - 1 >= p.prefix_len));
+        const uint32_t which = __ballot_sync(0xffffffffu, mine);
+        const int src = which ? __ffs(which) - 1 : 0;
+        const int32_t len = __shfl_sync(0xffffffffu, p.prefix_len, src), req = __shfl_sync(0xffffffffu, p.req, src);
+        if (which && ok) {
+            prefix = len;
+            preq = req;
+        }
+    }
     if (!ok) row.kv_end = 0;
-    const KeyRange kr = key_range(a, row, 0);
+    KeyRange kr = key_range(a, row, 0);
+    if (prefix > 0) {
+        const int32_t bs = a.block_size;
+        kr.lo = kr.sinks = prefix;
+        kr.shift = prefix / bs * bs - (prefix + bs - 1) / bs * bs;
+        kr.len = row.kv_end - kr.shift;
+    }
     PairItem it{};
     it.row = ri;
     it.req = row.req;
+    it.preq = preq;
     it.q_start = row.q_start;
     it.hk = unit - ri * a.hkv;
     it.sinks = kr.sinks;
     it.gap_end = kr.lo - kr.shift;
     it.shift = kr.shift;
     if (!ok && rank == 0 && it.hk == 0 && lane == 0) report_status(a.status, PCP_ERR_RANGE);
+    const int32_t tiles = (kr.len + kKeys - 1) / kKeys, chunk = max(1, (tiles + 2 * a.cluster - 1) / (2 * a.cluster)) * kKeys;
     int32_t n = 0;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-        it.lo = (2 * rank + w) * a.chunk;
-        it.hi = min(kr.len, it.lo + a.chunk);
+        it.lo = (2 * rank + w) * chunk;
+        it.hi = min(kr.len, it.lo + chunk);
         it.nt = it.hi > it.lo ? (it.hi - it.lo + kKeys - 1) / kKeys : 0;
         n += it.nt > 0;
         if (lane == 0) own[w] = it;
     }
-    *splits = (kr.len + a.chunk - 1) / a.chunk;
+    *splits = (kr.len + chunk - 1) / chunk;
     return n;
 }
 
@@ -369,7 +409,7 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
             const int32_t v = it.lo + j * kKeys + lane * bs;
             const int32_t pg = (v >= it.sinks ? v + it.shift : v) / bs;  // a page begun by sinks holds them
             if (lane * bs >= kKeys || v >= it.hi || pg >= a.max_blocks) return -1;
-            return __ldg(a.block_table + (size_t)it.req * a.max_blocks + pg);
+            return __ldg(a.block_table + (size_t)(v >= it.sinks ? it.req : it.preq) * a.max_blocks + pg);
         };
         bool ok = true;
         uint32_t gt = 0, uses[2] = {0, 0};  // tiles; items with a Q^T load per warpgroup
@@ -820,8 +860,9 @@ bool decode_inline_applies(const PrefillArgs& a, int32_t max_splits) {
            (int64_t)a.num_rows * a.hkv * max_splits <= 2 * a.num_sms;
 }
 
-// Blocks per row and kv head of a window call whose one-token rows (as many as tokens) a
-// cluster each can take side by side, and then in *chunk the keys per split; 0: none.
+// Blocks per row and kv head of a call whose one-token rows (as many as tokens) a
+// cluster each can take side by side; 0: none. max_splits and a.chunk: the splits that the
+// call would have otherwise.
 // Clusters that all run at once: 15 of 8 blocks, 36 of 4, 76 of 2 fit the 152 SMs (one
 // more and 1024-key windows take 18.5 us instead of 11.1, 22.6 instead of 14.3), a few
 // are left for GPCs with fewer SMs. Where they leave SMs idle, their splits are at most one
@@ -829,15 +870,20 @@ bool decode_inline_applies(const PrefillArgs& a, int32_t max_splits) {
 // one kv head takes 27.4 us in one cluster, 22.6 with 304 splits and a merge (but 64
 // such pairs of a row and a head, two blocks each, 85 against 95). One split per
 // row (max_splits 1) needs no joining.
-int32_t decode_cluster(const PrefillArgs& a, int64_t max_len, int32_t max_splits, int32_t* chunk) {
-    if (!decode_tc_applies(a) || a.num_prefixes > 0 || a.total_q > a.num_rows || max_splits == 1) return 0;
+// With shared prefixes every row reads its prefix itself, most of it from L2: with 2 to 32
+// rows, 1 to 8 kv heads and a bf16 cache 12 to 14 us instead of 23 to 25 behind 256 keys, 12 to 20
+// instead of 24 to 28 behind 1008, 25 to 27 instead of 28 to 37 with 1000 keys per split, 41
+// instead of 36 to 40 with 2000. Not over an e4m3 cache, where a prefix has the
+// descales of its group's request.
+int32_t decode_cluster(const PrefillArgs& a, int64_t max_len, int32_t max_splits) {
+    if (!decode_tc_applies(a) || a.total_q > a.num_rows || (max_splits == 1 && a.num_prefixes == 0)) return 0;
+    if (a.num_prefixes > kClusterGroups || (a.num_prefixes > 0 && a.k_descale)) return 0;
     const int64_t units = (int64_t)a.num_rows * a.hkv;
     for (int32_t c = kMaxCluster; c >= 1; c /= 2) {
         if ((units + 5) * c > a.num_sms) continue;
         const int64_t keys = (max_len + 2 * c * kKeys - 1) / (2 * c * kKeys) * kKeys;
-        if (units * c * 4 < a.num_sms * 3 && keys > *chunk + kKeys) return 0;
-        *chunk = (int32_t)keys;
-        return c;
+        if (a.num_prefixes > 0) return keys <= kPrefixKeys ? c : 0;
+        return units * c * 4 >= a.num_sms * 3 || keys <= a.chunk + kKeys ? c : 0;
     }
     return 0;
 }

@@ -1469,9 +1469,8 @@ __global__ void __launch_bounds__(NT, 1)
         if (r0 > 0 && ri < num_rows) row = a.rows[ri];
         int32_t cnt = 0, splits = 0, dec_tiles = 0, lo = 0, grp = -1;
         if (ri < num_rows) {
-            // (without prefixes the packed kernel is not launched for num_rows >= total_q)
-            bool ok = row_in_range(row, a.num_reqs, a.total_q, max_kv) &&
-                      (row.q_len == 1 || ng > 0 || a.total_q > num_rows);
+            // (a call with num_rows >= total_q takes one-token rows only)
+            bool ok = row_in_range(row, a.num_reqs, a.total_q, max_kv) && (row.q_len == 1 || a.total_q > num_rows);
             for (int32_t g = 0; g < ng && ok; ++g) {
                 const pcp_prefix_t p = prefix[g];
                 const int64_t p1 = (int64_t)p.q_start + p.q_len, r1 = (int64_t)row.q_start + row.q_len;

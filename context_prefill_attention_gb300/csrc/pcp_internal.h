@@ -273,8 +273,8 @@ int launch_range_decode(const PrefillArgs& a, float* dec_out, float* dec_lse, in
 // Whether a window call's rows are one-token rows (as many as tokens) few enough for
 // the decode kernel to find its items without the scheduler.
 bool decode_inline_applies(const PrefillArgs& a, int32_t max_splits);
-// Whether a cluster per row and kv head takes them: its blocks (0: no), and their keys per split.
-int32_t decode_cluster(const PrefillArgs& a, int64_t max_len, int32_t max_splits, int32_t* chunk);
+// Whether a cluster per row and kv head takes the rows: its blocks (0: no).
+int32_t decode_cluster(const PrefillArgs& a, int64_t max_len, int32_t max_splits);
 int launch_decode_pair(const PrefillArgs& a, float* dec_out, float* dec_lse, int32_t max_splits,
                        cudaStream_t stream);
 int launch_range_merge(const PrefillArgs& a, const MergeTask* tasks, const float* dec_out, const float* dec_lse,

@@ -227,7 +227,7 @@ int range_call(const RangeCall& c) {
     a.direct = !shared && w.max_splits == 1;
     MergeTask* tasks = reinterpret_cast<MergeTask*>(ws + w.merge);
     a.merge = tasks;
-    a.cluster = decode_cluster(a, max_len, w.max_splits, &a.chunk);
+    a.cluster = decode_cluster(a, max_len, w.max_splits);
     a.inline_items = a.cluster > 0 || decode_inline_applies(a, w.max_splits);
     int rc = PCP_OK;
     if (!a.inline_items)
@@ -242,7 +242,7 @@ int range_call(const RangeCall& c) {
     if (rc != PCP_OK) return rc;
     // no row can have two tokens when there are as many rows as tokens (the rows'
     // tokens are disjoint): only prefixes are left for the packed kernel
-    if (c.total_q > c.num_rows || a.num_prefixes > 0) {
+    if (c.total_q > c.num_rows || (a.num_prefixes > 0 && a.cluster == 0)) {
         rc = launch_packed(a, c.stream);
         if (rc != PCP_OK) return rc;
     }

@@ -415,7 +415,7 @@ int pcp_build_prefix_groups(const pcp_row_t* rows, int32_t num_rows, const int32
 /*
  * pcp_attn_shared_prefix — device. No counterpart on the pages: pcp_attn_varlen
  * (flags 0) for a batch in which groups of tokens share a prefix of their keys,
- * with each prefix's attention computed once for the whole group. A group's
+ * with each prefix's attention computed for the whole group at once. A group's
  * prefix is read once per tile of its tokens x q heads (tensor cores, the keys
  * split over the SMs), each row's own keys from prefix_len on as usual, and the
  * parts are merged by log-sum-exp in the call. The result is that of
@@ -426,9 +426,10 @@ int pcp_build_prefix_groups(const pcp_row_t* rows, int32_t num_rows, const int32
  * prefix (kv_end - q_len >= prefix_len). A group that breaks a rule is skipped
  * with its rows, as is such a row, with *status = PCP_ERR_RANGE. num_prefixes
  * in [0, 1024] (else PCP_ERR_ARG); with 0, prefixes may be NULL.
- * A row of one token takes the decode path whatever its is_decode.
- * With num_prefixes == 0 a call with num_rows >= total_q takes one-token rows
- * only (see pcp_attn_window). FP8 cache: the descales of a prefix are those of its req
+ * A row of one token takes the decode path whatever its is_decode, and a call
+ * with num_rows >= total_q takes one-token rows only (see pcp_attn_window). In
+ * small calls of one-token rows each row attends its prefix itself, where that is
+ * quicker, from the pages of the group's req. FP8 cache: the descales of a prefix are those of its req
  * (requests that share pages share descales); numerics of pcp_attn_window_fp8kv.
  * Every other argument, limit, check and error is that of pcp_attn_varlen; there
  * are no flags. workspace: at least pcp_attn_shared_prefix_workspace_size(

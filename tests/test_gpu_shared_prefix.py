@@ -38,6 +38,57 @@ def test_group_sizes(rows):
     b.check(*b.run())
 
 
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (3, 3), (16, 1), (16, 8)])
+@pytest.mark.parametrize("bs,share", [(8, True), (16, True), (16, False), (64, True), (128, False)])
+def test_few_rows_of_groups(hq, hkv, bs, share):
+    """Batches whose rows attend their prefixes themselves: prefixes that end at, before and
+    behind a page's or a tile's end, rows with one key of their own, rows of no group."""
+    P = _pcp()
+    for a, c in ((1, bs - 1), (bs, 127), (bs + 1, 129), (128, 1000), (1024 - bs, 1999)):
+        reqs = [(1, a), (1, a + 200), (1, 0), (1, 77), (1, c + 1), (1, c), (1, c + bs), (1, c + 300), (1, 260)]
+        if hkv < 8:
+            reqs += [(1, c + 33), (1, c)]
+        b = Batch(reqs, hq, hkv, 128, bs, groups=[(0, 2, a), (4, 4, c)] + ([(9, 2, c)] if hkv < 8 else []), seed=a + c,
+                  share_pages=share)
+        out, lse = b.run()
+        b.check(out, lse)
+        again, again_lse = b.run()
+        assert torch.equal(out, again) and torch.equal(lse, again_lse)
+
+
+@pytest.mark.parametrize("bad", [[0, 2, 0, 10 ** 6], [0, 2, 9, 640], [-1, 3, 0, 640], [0, 0, 0, 640], [0, 2, 0, 0],
+                                 [0, 2, 0, 641], [0, 3, 0, 640], [2, 2, 0, 640], [0, -1, 0, 640], [0, 2, -1, 640],
+                                 [2 ** 31 - 1, 2 ** 31 - 1, 0, 640]])
+def test_bad_groups_among_few_rows(bad):
+    """As below, with one-token rows only: rows of a bad group are left as they were, rows of
+    no group and of the other group stand."""
+    P = _pcp()
+    reqs = [(1, 640), (1, 660), (1, 640), (1, 680), (1, 30)]
+    b = Batch(reqs, 8, 2, 128, 16, groups=[(0, 2, 640), (2, 2, 640)], seed=2)
+    want, want_lse = b.run()
+    b.check(want, want_lse)
+    pre = b.prefixes.copy()
+    pre[0] = bad
+    out, lse = b.run(prefixes=pre)
+    torch.cuda.synchronize()
+    assert int(b.status.item()) == P.PCP_ERR_RANGE
+    assert torch.equal(out[4], want[4]) and torch.equal(lse[:, 4], want_lse[:, 4])
+    second_ok = bad[0] < 2 and bad[0] + max(bad[1], 0) <= 2  # the ranges ascend and are disjoint
+    for t in (2, 3):
+        assert torch.equal(out[t], want[t]) if second_ok else (out[t] == 7.0).all()
+    if bad == [0, 2, 0, 641]:  # row 0 begins before the prefix's end, row 1 does not
+        assert (out[0] == 7.0).all() and torch.isfinite(out[1]).all() and not (out[1] == 7.0).all()
+    elif bad[0] == 0 and bad[1] > 0 and bad != [0, 3, 0, 640]:
+        assert (out[:2] == 7.0).all()
+    # a row of two tokens, where there are as many rows as tokens
+    b.status.zero_()
+    b.rows_dev[0, 3] = 2
+    out, _ = b.run()
+    torch.cuda.synchronize()
+    assert int(b.status.item()) == P.PCP_ERR_RANGE
+    assert (out[0] == 7.0).all() and torch.equal(out[1:], want[1:])
+
+
 def test_long_prefix():
     reqs = [(1, 20000 + 3 * i) for i in range(6)]
     b = Batch(reqs, 8, 2, 128, 64, groups=[(0, 6, 20000)], seed=1)
