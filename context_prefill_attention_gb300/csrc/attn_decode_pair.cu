@@ -131,6 +131,19 @@ __device__ __forceinline__ PairItem pair_item(const PrefillArgs& a, int32_t p, i
 
 static_assert(sizeof(PairItem) == 44, "two of them fit at PairCfg::kOwn");
 
+// e4m3 cache: the V descales of an item's own keys and of those it walks as sinks (a shared
+// prefix's are its request's), as a factor at most 1 on P for each and one on the result.
+struct VScale {
+    float all, own, pre;
+};
+__device__ __forceinline__ VScale v_scale(const PrefillArgs& a, const PairItem& it) {
+    const float own = __ldg(a.v_descale + (size_t)it.req * a.hkv + it.hk);
+    const float pre = it.preq == it.req ? own : __ldg(a.v_descale + (size_t)it.preq * a.hkv + it.hk);
+    if (own == pre) return {own, 1.f, 1.f};
+    const float all = fmaxf(fabsf(own), fabsf(pre));
+    return {all, own / all, pre / all};
+}
+
 // a.inline_items: one warp's work of finding the items `p0` and `p1` (-1: none) among
 // all rows, splits and kv heads (row by row, split by split, head by head); returns
 // the item count. CTA 0 also reports bad rows and writes the merge records.
@@ -611,6 +624,13 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
             const int32_t n_other = item_at(2 * q + 1 - wg).nt;
             const float kd = F8 ? __ldg(a.k_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
             const float sl2 = a.scale * kd * kLog2e;
+            float sl2_pre = sl2, p_own = 1.f, p_pre = 1.f;
+            if (F8 && it.preq != it.req) {
+                const VScale f = v_scale(a, it);
+                p_own = f.own;
+                p_pre = f.pre;
+                sl2_pre = a.scale * __ldg(a.k_descale + (size_t)it.preq * a.hkv + it.hk) * kLog2e;
+            }
             // FP8: the power of two that undoes each head's q scaling (see q_to_e4m3_terms)
             float qs[GP];
 #pragma unroll
@@ -657,6 +677,8 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
                 const int32_t v0 = it.lo + j * kKeys;
                 const int nvalid = min(kKeys, it.hi - v0);
                 const bool valid = t < nvalid && it.live(v0 + t);
+                const bool pre = F8 && v0 + t < it.sinks;
+                const float p_up = 0x1p8f * (pre ? p_pre : p_own);
                 ok &= mbar_wait_warp(s_full(wg), c & 1, abort_flag);
                 tc_fence_after();
                 uint32_t s[kNS];
@@ -669,7 +691,7 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
                     if constexpr (F8) {  // the q terms' scores, then the head's q scale
                         sh = (sh + __uint_as_float(s[GP + h])) * qs[h];
                     }
-                    x[h] = valid ? sh * sl2 : -INFINITY;
+                    x[h] = valid ? sh * (pre ? sl2_pre : sl2) : -INFINITY;
                 }
                 // tile max per head: over the warp, then over the warpgroup's four warps
                 float* rm = red_m + (c & 1) * 4 * kGS;  // [warp][head]
@@ -688,17 +710,16 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
                     l_t[h] = l_t[h] * alpha + pe;
                     a_prev[h] = alpha;
                     if constexpr (F8) {
-                        float rem = pe;
+                        float term = pe * p_up;  // p 2^8, then the remainders 2^12 and 2^16
 #pragma unroll
                         for (int n = 0; n < 3; ++n) {
-                            const float up = n == 0 ? 0x1p8f : n == 1 ? 0x1p12f : 0x1p16f;
-                            const uint32_t code = f32x2_to_e4m3x2(rem * up, 0.f);
+                            const uint32_t code = f32x2_to_e4m3x2(term, 0.f);
                             const int row = n * kTS + h;
                             pcol[row * 128 + ((chunk ^ (row & 7)) << 4)] = (uint8_t)code;
                             if (n < 2) {
                                 float back[4];
                                 e4m3x4_to_f32(code, back);
-                                rem -= back[0] * (1.f / up);  // exact: both hold few significant bits
+                                term = (term - back[0]) * 16.f;  // exact: both hold few significant bits
                             }
                         }
                     } else {
@@ -735,7 +756,7 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
             float* rl = red_l + (q & 1) * 4 * kGS;  // [warp][head]
             const float wl = warp_scatter<GP, false>(l_t, lane);
             if (lane % kSpan == 0) rl[wq * kGS + hl] = wl;
-            const float vd = F8 ? __ldg(a.v_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
+            const float vd = F8 ? v_scale(a, it).all : 1.f;
             if ((stop = bar_wg_or(1 + wg, !ok))) break;
             if (a.cluster) {  // the split's sums for the cluster's merge, where its maxima and P were
                 float* part = reinterpret_cast<float*>(pbuf);
@@ -779,7 +800,7 @@ __global__ void __launch_bounds__(PairCfg<F8, GP>::kThreads, 1)
         if (warp < 8 && n > 0) {
             const int wg = warp / 4, t = threadIdx.x % 128;
             const PairItem it = own[0];
-            const float vd = F8 ? __ldg(a.v_descale + (size_t)it.req * a.hkv + it.hk) : 1.f;
+            const float vd = F8 ? v_scale(a, it).all : 1.f;
             const int32_t rank = (int32_t)blockIdx.x % a.cluster;
             for (int h = 2 * rank + wg; h < G; h += 2 * a.cluster) {
                 float m[2 * kMaxCluster], l[2 * kMaxCluster], x[2 * kMaxCluster];
@@ -873,11 +894,10 @@ bool decode_inline_applies(const PrefillArgs& a, int32_t max_splits) {
 // With shared prefixes every row reads its prefix itself, most of it from L2: with 2 to 32
 // rows, 1 to 8 kv heads and a bf16 cache 12 to 14 us instead of 23 to 25 behind 256 keys, 12 to 20
 // instead of 24 to 28 behind 1008, 25 to 27 instead of 28 to 37 with 1000 keys per split, 41
-// instead of 36 to 40 with 2000. Not over an e4m3 cache, where a prefix has the
-// descales of its group's request.
+// instead of 36 to 40 with 2000 (e4m3: 12 to 20 instead of 25 to 29 behind 1008 keys).
 int32_t decode_cluster(const PrefillArgs& a, int64_t max_len, int32_t max_splits) {
     if (!decode_tc_applies(a) || a.total_q > a.num_rows || (max_splits == 1 && a.num_prefixes == 0)) return 0;
-    if (a.num_prefixes > kClusterGroups || (a.num_prefixes > 0 && a.k_descale)) return 0;
+    if (a.num_prefixes > kClusterGroups) return 0;
     const int64_t units = (int64_t)a.num_rows * a.hkv;
     for (int32_t c = kMaxCluster; c >= 1; c /= 2) {
         if ((units + 5) * c > a.num_sms) continue;

@@ -40,7 +40,8 @@ def test_group_sizes(rows):
 
 @pytest.mark.parametrize("hq,hkv", [(4, 1), (3, 3), (16, 1), (16, 8)])
 @pytest.mark.parametrize("bs,share", [(8, True), (16, True), (16, False), (64, True), (128, False)])
-def test_few_rows_of_groups(hq, hkv, bs, share):
+@pytest.mark.parametrize("fp8", [False, True])
+def test_few_rows_of_groups(hq, hkv, bs, share, fp8):
     """Batches whose rows attend their prefixes themselves: prefixes that end at, before and
     behind a page's or a tile's end, rows with one key of their own, rows of no group."""
     P = _pcp()
@@ -49,11 +50,27 @@ def test_few_rows_of_groups(hq, hkv, bs, share):
         if hkv < 8:
             reqs += [(1, c + 33), (1, c)]
         b = Batch(reqs, hq, hkv, 128, bs, groups=[(0, 2, a), (4, 4, c)] + ([(9, 2, c)] if hkv < 8 else []), seed=a + c,
-                  share_pages=share)
+                  share_pages=share, fp8=fp8)
         out, lse = b.run()
         b.check(out, lse)
         again, again_lse = b.run()
         assert torch.equal(out, again) and torch.equal(lse, again_lse)
+
+
+@pytest.mark.parametrize("rows", [3, 7, 90])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (16, 2)])
+def test_descales_of_the_prefix_are_its_requests(rows, hq, hkv):
+    """e4m3 cache whose requests have descales of their own: a prefix takes those of the group's
+    request, a row's own keys the row's, of either sign and of zero."""
+    pre = 523
+    b = Batch([(1, pre + 60 * (i % 5)) for i in range(rows)], hq, hkv, 128, 16, fp8=True, groups=[(0, rows, pre)], seed=rows)
+    f = torch.tensor([[1.0, 1.5, -0.25, 0.0, 2.0, 0.5, -1.0], [1.0, -0.5, 3.0, 1.0, 0.0, -1.0, 0.125]])
+    for i, dev in enumerate((b.kd_dev, b.vd_dev)):
+        for r in range(1, rows):
+            x = float(f[i, r % 7])
+            dev[r] *= x
+            b.keys[i][r][pre:] *= x
+    b.check(*b.run())
 
 
 @pytest.mark.parametrize("bad", [[0, 2, 0, 10 ** 6], [0, 2, 9, 640], [-1, 3, 0, 640], [0, 0, 0, 640], [0, 2, 0, 0],
