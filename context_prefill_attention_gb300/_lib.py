@@ -419,8 +419,9 @@ def _i32_arg(x, name: str) -> int:
 def _ready(device: int, *pairs) -> bool:
     """Whether every ``(tensor, dtype)`` is a contiguous CUDA tensor of that type on
     that device (the quick form of :func:`_dev`, which says what is wrong)."""
+    kind = torch.Tensor
     for t, dtype in pairs:
-        if type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        if type(t) is not kind or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
             return False
     return True
 
@@ -586,15 +587,22 @@ def pcp_kv_pages_workspace_size(num_blocks: int) -> int:
     return int(load().pcp_kv_pages_workspace_size(num_blocks))
 
 
-def _have(t, dtype, device: int, shape) -> bool:
-    """Whether ``t`` is a contiguous CUDA tensor of that type, device and shape."""
-    return type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device and device >= 0 \
-        and t.shape == shape and t.is_contiguous()
+def _ints_ready(device: int, *pairs) -> bool:
+    """Whether every ``(tensor, shape)`` is a contiguous int32 CUDA tensor of that shape on
+    that device (the quick form of :func:`_i32_in`)."""
+    if device < 0:
+        return False
+    i32, kind = torch.int32, torch.Tensor
+    for t, shape in pairs:
+        if type(t) is not kind or t.dtype is not i32 or t.get_device() != device or t.shape != shape \
+                or not t.is_contiguous():
+            return False
+    return True
 
 
 def _i32_in(t, name: str, shape, like) -> None:
     """``t`` checked as an int32 input of ``shape`` on the device of ``like``."""
-    if not _have(t, torch.int32, like.get_device(), shape):
+    if not _ints_ready(like.get_device(), (t, shape)):
         _dev(t, name, I32, shape=shape, device=like.device)
 
 
@@ -607,7 +615,7 @@ def _i32_out(t, name: str, shape, like):
 
 
 def _status_in(status, like) -> None:
-    if status is not None and not (_have(status, torch.int32, like.get_device(), (1,))):
+    if status is not None and not _ints_ready(like.get_device(), (status, (1,))):
         _status(status, like.device)
 
 
@@ -649,11 +657,12 @@ def pcp_kv_fork(key_cache: torch.Tensor, value_cache: torch.Tensor, block_table:
     lib = load()
     dev, nb, bs, slot_bytes = _check_pages(key_cache, value_cache, block_table, ref_count, status)
     R, mb = block_table.shape
-    _i32_in(kv_len, "kv_len", (R,), block_table)
     N = parent.numel() if isinstance(parent, torch.Tensor) else 0
-    _i32_in(parent, "parent", (N,), block_table)
-    block_table_out = _i32_out(block_table_out, "block_table_out", (N, mb), block_table)
-    ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
+    if not _ints_ready(dev, (kv_len, (R,)), (parent, (N,)), (block_table_out, (N, mb)), (ref_count_out, (nb,))):
+        _i32_in(kv_len, "kv_len", (R,), block_table)
+        _i32_in(parent, "parent", (N,), block_table)
+        block_table_out = _i32_out(block_table_out, "block_table_out", (N, mb), block_table)
+        ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
     workspace = _pages_workspace(workspace, nb, block_table)
     rc = _launch(lib.pcp_kv_fork, dev, stream, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, slot_bytes,
                  block_table.data_ptr(), R, mb, kv_len.data_ptr(), parent.data_ptr(), N, ref_count.data_ptr(),
@@ -676,13 +685,15 @@ def pcp_kv_release(block_table: torch.Tensor, first_page: torch.Tensor, last_pag
     if dev < 0 or block_table.dim() != 2 or not _ready(dev, (block_table, torch.int32)):
         _dev(block_table, "block_table", I32, shape=(-1, -1))
     R, mb = block_table.shape
-    _i32_in(first_page, "first_page", (R,), block_table)
-    _i32_in(last_page, "last_page", (R,), block_table)
     nb = ref_count.numel() if isinstance(ref_count, torch.Tensor) else 0
-    _i32_in(ref_count, "ref_count", (nb,), block_table)
+    if not _ints_ready(dev, (first_page, (R,)), (last_page, (R,)), (ref_count, (nb,)), (block_table_out, (R, mb)),
+                       (ref_count_out, (nb,))):
+        _i32_in(first_page, "first_page", (R,), block_table)
+        _i32_in(last_page, "last_page", (R,), block_table)
+        _i32_in(ref_count, "ref_count", (nb,), block_table)
+        block_table_out = _i32_out(block_table_out, "block_table_out", (R, mb), block_table)
+        ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
     _status_in(status, block_table)
-    block_table_out = _i32_out(block_table_out, "block_table_out", (R, mb), block_table)
-    ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
     rc = _launch(lib.pcp_kv_release, dev, stream, block_table.data_ptr(), R, mb,
                  first_page.data_ptr(), last_page.data_ptr(), ref_count.data_ptr(), nb, block_table_out.data_ptr(),
                  ref_count_out.data_ptr(), None if status is None else status.data_ptr())
@@ -701,9 +712,10 @@ def pcp_kv_compact(key_cache: torch.Tensor, value_cache: torch.Tensor, block_tab
     lib = load()
     dev, nb, bs, slot_bytes = _check_pages(key_cache, value_cache, block_table, ref_count, status)
     R, mb = block_table.shape
-    block_table_out = _i32_out(block_table_out, "block_table_out", (R, mb), block_table)
-    ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
-    num_live = _i32_out(num_live, "num_live", (1,), block_table)
+    if not _ints_ready(dev, (block_table_out, (R, mb)), (ref_count_out, (nb,)), (num_live, (1,))):
+        block_table_out = _i32_out(block_table_out, "block_table_out", (R, mb), block_table)
+        ref_count_out = _i32_out(ref_count_out, "ref_count_out", (nb,), block_table)
+        num_live = _i32_out(num_live, "num_live", (1,), block_table)
     workspace = _pages_workspace(workspace, nb, block_table)
     rc = _launch(lib.pcp_kv_compact, dev, stream, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, slot_bytes,
                  block_table.data_ptr(), R, mb, ref_count.data_ptr(), block_table_out.data_ptr(),
