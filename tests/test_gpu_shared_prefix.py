@@ -164,6 +164,53 @@ def test_streams_graphs_and_repeats():
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_few_rows_on_two_streams_and_in_a_graph(fp8):
+    """Calls of one kernel: side by side on two streams, and captured, with the rows and groups
+    changed in place between replays."""
+    P = _pcp()
+    a = Batch([(1, 700 + 90 * i) for i in range(8)], 8, 2, 128, 16, fp8=fp8, groups=[(0, 8, 700)], seed=3)
+    w = Batch([(1, 400 * i) for i in range(12)], 8, 2, 128, 16, fp8=fp8, window=900, sinks=4, seed=4)
+    first, second = a.run(), w.run()
+    a.check(*first)
+    w.check(*second)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for b, s in zip((a, w), streams):
+            with torch.cuda.stream(s):
+                got.append(b.run())
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        want = (first, second)[i % 2]
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    out, lse = a.buffers()
+    ws = torch.empty(P.pcp_attn_shared_prefix_workspace_size(8, 1, a.T, 8, 2, 128, a.table.shape[1] * 16),
+                     dtype=torch.uint8, device="cuda")
+    pre = torch.from_numpy(a.prefixes).cuda()
+    f = P.pcp_attn_shared_prefix_fp8kv if fp8 else P.pcp_attn_shared_prefix
+    descales = (a.kd_dev, a.vd_dev) if fp8 else ()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f(a.q_dev, a.kc, a.vc, *descales, a.table_dev, a.rows_dev, pre, a.scale, out=out, lse=lse, workspace=ws,
+          status=a.status)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    # a shorter prefix, or fewer rows in the group, give the same attention
+    pre[0, 3] = 320
+    out.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    a.check(out, lse)
+    pre[0, 1] = 5
+    out.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    a.check(out, lse)
+
+
 @pytest.mark.parametrize("bad", [[0, 3, 0, 10 ** 6], [0, 3, 9, 640], [-1, 4, 0, 640], [0, 0, 0, 640], [0, 9, 0, 640],
                                  [0, 3, 0, 0], [0, 2, 0, 700], [0, 1, 0, 640]])
 def test_bad_groups_are_reported(bad):
